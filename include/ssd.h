@@ -421,6 +421,146 @@ ssd_status ssd_discretize(const ssd_problem* p, const float* dt, const float* dt
 ssd_status ssd_decode_step(const ssd_problem* p, const void* x, const float* log_a, const void* B, const void* C,
                            const float* D, float* state, void* y, void* stream);
 
+/* ---- around the scan: short convolution, selective scan, norms ----
+ * The parts of a state-space block next to its scan: the short causal
+ * convolution before it, the older selective scan with a decay per channel and
+ * state, the norm with its gate after the mixer and the norm before a block
+ * with its residual sum (ai.tomabc.com "Mamba": the block pseudocode, linear ->
+ * conv1d -> silu -> SSM -> gate; awesome.papernotes.org, design 3: the extra norm
+ * before the output projection). The conventions above hold, and:
+ *  - Activations are slices of a projection's output as often as tensors of
+ *    their own, so the inputs named "strided" may have any batch and token
+ *    stride (in elements, >= 0); their channels are contiguous. They, and every
+ *    output, need only the alignment of one element: 16-byte accesses are used
+ *    where all addresses and strides allow them. Outputs are dense. Parameters
+ *    (weight, bias, A, D, dt_bias, scale) and scan states are fp32.
+ *  - An output that overlaps an input or another output in memory is
+ *    SSD_ERR_INVALID_ARG (in-place state buffers apart); where an input is
+ *    strided, what lies between its rows counts as part of it.
+ *  - Sums, statistics and states are fp32; each output is rounded once.
+ *  - batch * seqlen <= 2^31 - 1, channels <= 2^20, nseq <= 2^24, else
+ *    SSD_ERR_UNSUPPORTED. */
+
+typedef enum {
+    SSD_ACT_NONE = 0,
+    SSD_ACT_SILU = 1   /* silu(v) = v / (1 + exp(-v)) */
+} ssd_activation;
+
+typedef struct {
+    int64_t batch, seqlen;
+    int64_t channels;
+    int64_t width;        /* W: taps, 2, 3 or 4 */
+    int64_t nseq;         /* sequences per batch row: 1 when seq_idx is NULL */
+    int64_t x_stride[2];  /* elements from one batch row / one token of x to the next */
+    int64_t split[3];     /* channels of out0, out1, out2 in order, summing to channels;
+                             0 behind the last used output */
+    ssd_dtype dtype;      /* of x, the outputs and the windows */
+    ssd_activation act;
+} ssd_conv_problem;
+
+/* ssd_causal_conv: the short causal convolution of every channel with its own
+ * taps, restarted at every sequence:
+ *   y[b, t, c] = act(bias[c] + sum_{k < W} weight[c, k] * in[b, t - (W - 1) + k, c])
+ * where in[b, t'] is x[b, t'] for a token t' of t's sequence, and for the j-th
+ * token before that sequence's first (j = 1 .. W-1) the initial window's entry
+ * init_states[b, s, W-1-j] (0 when init_states is NULL). final_states[b, s] is the
+ * window after the last token of sequence s, the last W-1 inputs, oldest first;
+ * ids that do not occur in a row keep their initial window (or zero).
+ *   x             [batch, seqlen, channels]        dtype, strided
+ *   weight        [channels, W] fp32               bias [channels] fp32 or NULL
+ *   init_states   [batch, nseq, W-1, channels]     dtype or NULL
+ *   seq_idx       [batch, seqlen]                  int32 or NULL (one sequence)
+ *   out0..out2    [batch, seqlen, split[i]]        dtype, out: y's channels in
+ *                                                  order (for ssd_fwd: x, B, C);
+ *                                                  NULL where split[i] is 0
+ *   final_states  [batch, nseq, W-1, channels]     dtype, out, or NULL */
+ssd_status ssd_causal_conv(const ssd_conv_problem* p, const void* x, const float* weight, const float* bias,
+                           const void* init_states, const int32_t* seq_idx, void* out0, void* out1, void* out2,
+                           void* final_states, void* stream);
+
+/* ssd_conv_step: the same for one token of every batch row, its window updated
+ * in place (state[b] <- the last W-1 of state[b], x[b]). seqlen, nseq and
+ * x_stride[1] are not read.
+ *   x [batch, channels] dtype, strided (x_stride[0])
+ *   state [batch, W-1, channels] dtype, read and written   out0..out2 [batch, split[i]] */
+ssd_status ssd_conv_step(const ssd_conv_problem* p, const void* x, const float* weight, const float* bias,
+                         void* state, void* out0, void* out1, void* out2, void* stream);
+
+typedef struct {
+    int64_t batch, seqlen;
+    int64_t channels;      /* a multiple of ngroups: channel c uses group c*G/channels */
+    int64_t dstate;        /* N: 1 .. 256 */
+    int64_t ngroups;       /* G */
+    int64_t nseq;          /* sequences per batch row: 1 when seq_idx is NULL */
+    int64_t u_stride[2], dt_stride[2], z_stride[2];  /* batch row / token, in elements */
+    int64_t B_stride[2], C_stride[2];
+    ssd_dtype dtype;       /* of u, dt, B, C, z and y */
+    int32_t dt_softplus;   /* nonzero: delta = softplus(dt + dt_bias), else dt + dt_bias */
+} ssd_selective_problem;
+
+/* ssd_selective_scan: the selective scan with a decay per channel and state.
+ * For every row b, channel c and state n, with g = c*G/channels:
+ *   delta = softplus(dt[b, t, c] + dt_bias[c])   (or without the softplus)
+ *   h_t[n] = exp(delta A[c, n]) h_{t-1}[n] + delta u[b, t, c] B[b, t, g, n]
+ *   y[b, t, c] = (sum_n C[b, t, g, n] h_t[n] + D[c] u[b, t, c]) * silu(z[b, t, c])
+ * (ai.tomabc.com "Mamba": the selective SSM of the block pseudocode). Sequences,
+ * initial and final states are those of ssd_fwd.
+ *   u, dt, z      [batch, seqlen, channels]          dtype, strided; z may be NULL (no gate)
+ *   A             [channels, N] fp32 (<= 0 is the tested domain)
+ *   B, C          [batch, seqlen, G, N]              dtype, strided (G*N contiguous)
+ *   D, dt_bias    [channels] fp32 or NULL (= 0)
+ *   init_states   [batch, nseq, N, channels]         fp32 or NULL (= 0)
+ *   seq_idx       [batch, seqlen]                    int32 or NULL (one sequence)
+ *   y             [batch, seqlen, channels]          dtype, out
+ *   final_states  [batch, nseq, N, channels]         fp32, out, or NULL
+ *   workspace     >= ssd_selective_scan_workspace_bytes(p) bytes, 16-byte aligned
+ *                 (may be NULL when that is 0); contents are ignored and
+ *                 overwritten, and calls that may overlap need one each */
+size_t ssd_selective_scan_workspace_bytes(const ssd_selective_problem* p);  /* (size_t)-1 on invalid p */
+ssd_status ssd_selective_scan(const ssd_selective_problem* p, const void* u, const void* dt, const float* A,
+                              const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
+                              const float* init_states, const int32_t* seq_idx, void* y, float* final_states,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ssd_selective_step: the same for one token of every batch row, with the state
+ * updated in place. seqlen, nseq and the token strides are not read.
+ *   u, dt, z [batch, channels], B, C [batch, G, N]: dtype, strided (stride[0])
+ *   state [batch, N, channels] fp32, read and written     y [batch, channels] */
+ssd_status ssd_selective_step(const ssd_selective_problem* p, const void* u, const void* dt, const float* A,
+                              const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
+                              float* state, void* y, void* stream);
+
+typedef struct {
+    int64_t batch, seqlen;
+    int64_t channels;        /* a multiple of ngroups; channels / ngroups <= 32768 */
+    int64_t ngroups;         /* groups normalised on their own (ssd_add_norm: 1) */
+    int64_t x_stride[2];     /* batch row / token, in elements */
+    int64_t z_stride[2];     /* of z (ssd_gated_norm) or the residual (ssd_add_norm) */
+    ssd_dtype dtype;         /* of x, z and out */
+    ssd_dtype residual_dtype;/* of residual and residual_out: fp32 or dtype */
+    float eps;               /* >= 0 */
+    float alpha;             /* ssd_add_norm: host factor on x */
+    int32_t gate_first;      /* ssd_gated_norm: gate before the norm, else after it */
+} ssd_norm_problem;
+
+/* ssd_gated_norm: the norm after the mixer, over each group of channels,
+ *   v = x silu(z),  out = weight v / sqrt(mean_group(v^2) + eps)          (gate_first)
+ *   out = silu(z) weight x / sqrt(mean_group(x^2) + eps)                  (else)
+ * and without z the plain norm. x, z [batch, seqlen, channels] dtype, strided;
+ * weight [channels] fp32; out [batch, seqlen, channels] dtype. */
+ssd_status ssd_gated_norm(const ssd_norm_problem* p, const void* x, const void* z, const float* weight, void* out,
+                          void* stream);
+
+/* ssd_add_norm: the norm before a block, with the residual sum,
+ *   r = residual + alpha scale[c] x,   out = weight r / sqrt(mean(r^2) + eps)
+ * The norm takes r in fp32; residual_out is r rounded to residual_dtype.
+ * x [batch, seqlen, channels] dtype, strided; scale [channels] fp32 or NULL (= 1);
+ * residual [batch, seqlen, channels] residual_dtype, strided (z_stride), or NULL
+ * (= 0); out dtype, residual_out residual_dtype, both [batch, seqlen, channels].
+ * residual_out may be the residual itself where that is dense (in place). */
+ssd_status ssd_add_norm(const ssd_norm_problem* p, const void* x, const void* residual, const float* weight,
+                        const float* scale, void* out, void* residual_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

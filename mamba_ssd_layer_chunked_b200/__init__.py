@@ -43,6 +43,15 @@ from .ssd import (  # noqa: F401
     workspace_bytes,
 )
 
+from .block import declare as _declare_block  # noqa: E402
+from .block import (  # noqa: F401,E402
+    add_norm,
+    causal_conv,
+    conv_step,
+    gated_norm,
+    selective_scan,
+    selective_step,
+)
 from .sp import ssd_fwd_sp, torch_collectives  # noqa: F401,E402
 
-lib()  # fail loudly at import when the CUDA library is missing
+_declare_block(lib())  # fail loudly at import when the CUDA library is missing

@@ -11,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -49,14 +50,16 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
               "-I", INCLUDE, "-I", CSRC, "--expt-relaxed-constexpr"]
     if ptxas_verbose:
         common += ["-Xptxas", "-v"]
-    objs = []
-    for src in sources():
+    def compile_one(src: str) -> str:
         obj = os.path.join(objdir, os.path.basename(src) + ".o")
         cmd = common + ["-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-        objs.append(obj)
+        return obj
+
+    with ThreadPoolExecutor(max_workers=os.cpu_count() or 1) as pool:  # one nvcc per source
+        objs = list(pool.map(compile_one, sources()))
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     if verbose:

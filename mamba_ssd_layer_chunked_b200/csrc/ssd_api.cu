@@ -3,13 +3,12 @@
 // sequence chunk_cumsum -> chunk_state -> state_passing -> chunk_scan on the
 // caller's stream. Nothing here allocates, synchronises or reads device memory.
 
-#include <nvtx3/nvToolsExt.h>
-
 #include <atomic>
 #include <cstdio>
 #include <cstring>
 
 #include "ssd_common.cuh"
+#include "ssd_host.cuh"
 #include "ssd_tc.cuh"
 
 // The library's device error word: a kernel whose bounded wait gives up ORs a
@@ -37,29 +36,42 @@ cudaError_t device_error_word(unsigned int** out) {
     return cudaSuccess;
 }
 
-}  // namespace ssd
-
 namespace {
-
 thread_local char g_cuda_err[256] = "";
-
-// An NVTX range around the host-side enqueue of one entry point or one kernel
-// launch, named after it ("ssd_fwd", "fused_scan", ...): a profiler attaches
-// the kernels launched inside a range to its name (Nsight Systems' timeline,
-// `ncu --nvtx --nvtx-include`). With no tool attached a push or pop costs one
-// check of a function pointer.
-struct TraceRange {
-    explicit TraceRange(const char* name) { nvtxRangePushA(name); }
-    ~TraceRange() { nvtxRangePop(); }
-    TraceRange(const TraceRange&) = delete;
-    TraceRange& operator=(const TraceRange&) = delete;
-};
+}
 
 ssd_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return SSD_OK;
     std::snprintf(g_cuda_err, sizeof(g_cuda_err), "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
     return SSD_ERR_CUDA;
 }
+
+// The build targets sm_100a only: the device must be compute capability 10.0.
+// Also binds the calling thread to its current device's primary context: this
+// library carries its own CUDA runtime, so a host thread that has not used it
+// before (a thread per rank, say) would otherwise reach the first launch
+// without a current context.
+ssd_status check_device() {
+    int dev = 0, major = 0, minor = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SSD_ERR_UNSUPPORTED;
+    }
+    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return SSD_ERR_UNSUPPORTED;
+    }
+    return (major == 10 && minor == 0) ? SSD_OK : SSD_ERR_UNSUPPORTED;
+}
+
+}  // namespace ssd
+
+namespace {
+
+using ssd::check_device;
+using ssd::cuda_status;
+using ssd::TraceRange;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -83,25 +95,6 @@ ssd_status check_dims(const ssd_problem* p) {
     if (p->batch * p->nheads * nchunks * 4 > INT32_MAX) return SSD_ERR_UNSUPPORTED;
     if (p->batch * p->seqlen > INT32_MAX) return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
-}
-
-// The build targets sm_100a only: the device must be compute capability 10.0.
-// Also binds the calling thread to its current device's primary context: this
-// library carries its own CUDA runtime, so a host thread that has not used it
-// before (a thread per rank, say) would otherwise reach the first launch
-// without a current context.
-ssd_status check_device() {
-    int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
-        cudaGetLastError();
-        return SSD_ERR_UNSUPPORTED;
-    }
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return SSD_ERR_UNSUPPORTED;
-    }
-    return (major == 10 && minor == 0) ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
 ssd::Dims make_dims(const ssd_problem* p) {
@@ -271,7 +264,7 @@ const char* ssd_status_string(ssd_status s) {
     return "unknown status";
 }
 
-const char* ssd_last_cuda_error_string(void) { return g_cuda_err; }
+const char* ssd_last_cuda_error_string(void) { return ssd::g_cuda_err; }
 
 ssd_status ssd_device_error(uint32_t* code, void* stream) {
     ssd_status s = check_device();

@@ -1,0 +1,158 @@
+// ssd_norm.cu -- the norms of a block, each with what a block does around it:
+// the gated norm after the mixer and the norm before a block with its residual
+// sum.
+//
+//   gated:  v = x silu(z), out = w v / sqrt(mean_group v^2 + eps)   (or the gate after the norm)
+//   add:    r = residual + alpha scale x, out = w r / sqrt(mean r^2 + eps), r returned
+//
+// Source: "Mamba-2" (awesome.papernotes.org), design 3: the extra norm before
+// the output projection, after the gate of the Mamba block (ai.tomabc.com).
+//
+// Bound by bytes: every operand once. A CTA holds one row's group in registers
+// (up to 32 channels per thread), so the sum of squares and the scaled output
+// need one read. Sums: fp32 per thread, then a fixed tree over the CTA.
+
+#include "ssd_block.cuh"
+
+namespace ssd {
+
+namespace {
+
+constexpr int kNormMaxThreads = 1024;
+
+// The CTA's sum of v in a fixed order (same result on every thread).
+__device__ __forceinline__ float cta_sum(float v) {
+    __shared__ float part[32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int warps = blockDim.x / 32;
+    if (warps == 1) return v;
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = (int)(threadIdx.x % 32) < warps ? part[threadIdx.x % 32] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// One CTA per (row, group); thread i takes the group's vectors i, i + threads, ...
+// (NV of them at most). R: type of the residual (mode add).
+template <typename T, typename R, int V, int NV, int kMode>
+__global__ void __launch_bounds__(kNormMaxThreads) row_norm_kernel(const NormArgs a, int group, int nvec) {
+    const int row = blockIdx.x / a.ngroups, g = blockIdx.x % a.ngroups;
+    const int b = row / a.seqlen, t = row - b * a.seqlen;
+    const int c0 = g * group;
+    const T* x = static_cast<const T*>(a.x) + b * a.xs_b + t * a.xs_t + c0;
+    const T* z = static_cast<const T*>(a.z) + b * a.zs_b + t * a.zs_t + c0;
+    const R* res = static_cast<const R*>(a.z) + b * a.zs_b + t * a.zs_t;
+    const int64_t o = (int64_t)row * a.channels + c0;
+    Pack<T, V> xv[NV], zv[kMode == kNormGateFirst || kMode == kNormGateLast ? NV : 1];
+    Pack<R, V> rv[kMode == kNormAdd ? NV : 1];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = threadIdx.x + k * blockDim.x;
+        if (i >= nvec) break;
+        xv[k] = reinterpret_cast<const Pack<T, V>*>(x)[i];
+        if constexpr (kMode == kNormGateFirst || kMode == kNormGateLast)
+            zv[k] = reinterpret_cast<const Pack<T, V>*>(z)[i];
+        if constexpr (kMode == kNormAdd) {
+            if (a.z) rv[k] = reinterpret_cast<const Pack<R, V>*>(res)[i];
+        }
+    }
+    float v[NV][V], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = threadIdx.x + k * blockDim.x;
+        if (i >= nvec) break;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float f = to_f32(xv[k].v[e]);
+            if constexpr (kMode == kNormGateFirst) f *= silu_for<T>(to_f32(zv[k].v[e]));
+            if constexpr (kMode == kNormAdd) {
+                f *= a.scale ? a.alpha * a.scale[i * V + e] : a.alpha;
+                if (a.z) f += to_f32(rv[k].v[e]);
+            }
+            v[k][e] = f;
+            ss = fmaf(f, f, ss);
+        }
+        if constexpr (kMode == kNormAdd) {
+            Pack<R, V> ro;
+#pragma unroll
+            for (int e = 0; e < V; ++e) ro.v[e] = from_f32<R>(v[k][e]);
+            reinterpret_cast<Pack<R, V>*>(static_cast<R*>(a.residual_out) + o)[i] = ro;
+        }
+    }
+    const float inv = 1.f / sqrtf(cta_sum(ss) / (float)group + a.eps);
+    T* out = static_cast<T*>(a.out) + o;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int i = threadIdx.x + k * blockDim.x;
+        if (i >= nvec) break;
+        const Pack<float, V> w = reinterpret_cast<const Pack<float, V>*>(a.weight + c0)[i];
+        Pack<T, V> y;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float f = v[k][e] * inv * w.v[e];
+            if constexpr (kMode == kNormGateLast) f *= silu_for<T>(to_f32(zv[k].v[e]));
+            y.v[e] = from_f32<T>(f);
+        }
+        reinterpret_cast<Pack<T, V>*>(out)[i] = y;
+    }
+}
+
+template <typename T, typename R, int V, int NV, int kMode>
+cudaError_t run(const NormArgs& a, int group, int nvec, cudaStream_t st) {
+    const int threads = ((nvec + NV - 1) / NV + 31) / 32 * 32;
+    const unsigned grid = (unsigned)((int64_t)a.batch * a.seqlen * a.ngroups);
+    row_norm_kernel<T, R, V, NV, kMode><<<grid, threads, 0, st>>>(a, group, nvec);
+    return cudaGetLastError();
+}
+
+// vectors per thread: the fewest that 1024 threads allow
+template <typename T, typename R, int V, int kMode>
+cudaError_t by_count(const NormArgs& a, int group, cudaStream_t st) {
+    const int nvec = group / V;
+    if constexpr (V > 1) {
+        if (nvec <= kNormMaxThreads) return run<T, R, V, 1, kMode>(a, group, nvec, st);
+        if (nvec <= 2 * kNormMaxThreads) return run<T, R, V, 2, kMode>(a, group, nvec, st);
+        return run<T, R, V, 32 / V, kMode>(a, group, nvec, st);
+    } else {
+        if (nvec <= 4 * kNormMaxThreads) return run<T, R, V, 4, kMode>(a, group, nvec, st);
+        return run<T, R, V, 32, kMode>(a, group, nvec, st);
+    }
+}
+
+template <typename T, typename R, int kMode>
+cudaError_t by_access(const NormArgs& a, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const int group = a.channels / a.ngroups;
+    // the residual and the parameters may be wider than x: then V of them are two accesses
+    VectorRule r(sizeof(T)), q(sizeof(R)), w(sizeof(float));
+    r.address(a.x).address(a.out).elements(a.xs_b).elements(a.xs_t).elements(group);
+    q.elements(group);
+    if (a.z) q.address(a.z).elements(a.zs_b).elements(a.zs_t);
+    if (kMode == kNormAdd) q.address(a.residual_out);
+    w.address(a.weight);
+    const bool vec = r.multiple_of(16) && q.multiple_of(sizeof(Pack<R, V>) < 16 ? sizeof(Pack<R, V>) : 16) && w.multiple_of(16);
+    return vec ? by_count<T, R, V, kMode>(a, group, st) : by_count<T, R, 1, kMode>(a, group, st);
+}
+
+template <typename T>
+cudaError_t by_mode(const NormArgs& a, ssd_dtype residual_dt, cudaStream_t st) {
+    switch (a.mode) {
+        case kNormPlain: return by_access<T, T, kNormPlain>(a, st);
+        case kNormGateFirst: return by_access<T, T, kNormGateFirst>(a, st);
+        case kNormGateLast: return by_access<T, T, kNormGateLast>(a, st);
+        default:
+            return residual_dt == SSD_DTYPE_F32 ? by_access<T, float, kNormAdd>(a, st)
+                                                : by_access<T, T, kNormAdd>(a, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_row_norm(const NormArgs& a, ssd_dtype dt, ssd_dtype residual_dt, cudaStream_t st) {
+    return dt == SSD_DTYPE_F32 ? by_mode<float>(a, residual_dt, st) : by_mode<__nv_bfloat16>(a, residual_dt, st);
+}
+
+}  // namespace ssd
