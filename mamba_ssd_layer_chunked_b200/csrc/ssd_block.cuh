@@ -26,6 +26,7 @@ struct SelectiveArgs {
     int batch, seqlen, channels, dstate, ngroups, nseq;
     int64_t us_b, us_t, ds_b, ds_t, zs_b, zs_t, bs_b, bs_t, cs_b, cs_t;
     int softplus;
+    int bc_vectors;  // B and C rows allow 16-byte loads (set by the launcher)
     const void *u, *dt, *B, *C, *z;
     const float *A, *D, *dt_bias;
     const float* init;  // ssd_selective_step: the state, read and written
