@@ -26,7 +26,6 @@ struct SelectiveArgs {
     int batch, seqlen, channels, dstate, ngroups, nseq;
     int64_t us_b, us_t, ds_b, ds_t, zs_b, zs_t, bs_b, bs_t, cs_b, cs_t;
     int softplus;
-    int bc_vectors;  // B and C rows allow 16-byte loads (set by the launcher)
     const void *u, *dt, *B, *C, *z;
     const float *A, *D, *dt_bias;
     const float* init;  // ssd_selective_step: the state, read and written
@@ -73,7 +72,10 @@ __device__ __forceinline__ float silu_for<float>(float v) {
 }
 template <>
 __device__ __forceinline__ float silu_for<__nv_bfloat16>(float v) {
-    return __fdividef(v, 1.f + __expf(-v));
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return v * r;
 }
 
 // Largest number of channels per access (16-byte, 4-byte or one element) that

@@ -13,12 +13,14 @@
 // states each in registers, and a CTA's K warps take consecutive slices of
 // kSlice tokens, so that the exponentials of K * kSlice tokens are formed at
 // once although the recurrence is sequential. Over a slice the recurrence is
-// affine, h_end = P h_start + E: each warp forms its a = exp(delta A) (kept in
-// registers), E and P, the warps exchange (E, P) once per tile through shared
-// memory, each chains the slices before its own, and walks its slice again from
-// the true state, with the kept a, for the read-out. Every exponential is formed
+// affine in the state before it: with the local state (from zero) l_t and the
+// decay p_t since the slice's start, h_t = l_t + p_t h_start, so
+//   y_t = C_t . l_t + (C_t p_t) . h_start.
+// Each warp walks its slice once, keeping C_t p_t in registers, the warps
+// exchange (l_end, p_end) once per tile through shared memory, each chains the
+// slices before its own, and adds the second term. Every exponential is formed
 // once. Bound by the special-function unit (one exponential per (token,
-// channel, state)), then by the issue rate.
+// channel, state)) and the issue rate together.
 
 #include "ssd_block.cuh"
 
@@ -28,7 +30,6 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSlice = 8;       // tokens per warp and tile
-constexpr int kPairStride = 20; // floats between channels' (delta, delta u) rows: 16 used, conflict-free
 
 // 2^x, the hardware approximation (denormal results flushed to 0)
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -56,27 +57,68 @@ __device__ __forceinline__ float softplus(float z) {
 }
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
 
-// Lane = state slice * CPW + channel, CPW = 32 / LN channels per warp; a lane
-// holds states [ns * S, ns * S + S) of its channel. For loading inputs and
-// storing outputs a lane owns kSlice / LN tokens of its channel (one, shared by
-// LN / kSlice lanes, where LN > kSlice): those whose read-out it ends up with.
-template <typename T, int S, int LN, int K, bool kSeq>
+// Asynchronous copy of `bytes` bytes (2, 4, ... kBytes) to shared memory, zeros behind them.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
+    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+    if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(bytes), "n"(kBytes)
+                     : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+constexpr int kStages = 3;  // slices of raw inputs in shared memory: two in flight behind the current one
+
+// Layout of the scan's shared memory and its copies, for S states per lane, LN
+// lanes per channel, K warps.
+template <typename T, int S, int LN, int K>
+struct ScanShape {
+    static constexpr int CPW = 32 / LN;                                // channels per warp
+    static constexpr int NP = S * LN;                                  // states, padded
+    static constexpr int E = (int)sizeof(T);
+    static constexpr int TPL = LN < kSlice ? kSlice / LN : 1;          // tokens owned by a lane
+    static constexpr int SHARE = LN > kSlice ? LN / kSlice : 1;        // lanes that own the same token
+    static constexpr int ROW = CPW * E;                                // bytes of a token's channels
+    static constexpr int TB = ROW < 16 ? ROW : 16;                     // bytes per copy of u, dt, z
+    static constexpr int TR = (3 * kSlice * ROW / TB + 31) / 32;       // such copies per lane and slice
+    static constexpr int BV = 16 / E;                                  // B, C elements per copy
+    static constexpr int BR = kSlice * 2 * NP / BV / 32;               // such copies per lane and slice
+    static constexpr bool kCanCopy = TB >= 4 && NP >= BV && BR >= 1 && BR <= 4;
+    static constexpr int PAIR = CPW * (kSlice * 4 + 4);                // floats: (delta, delta, du, du) per token
+    static constexpr int BC = kSlice * 2 * NP;                         // floats: B and C of the slice
+    static constexpr int RAW = 3 * kSlice * ROW + BC * E;              // bytes of a raw stage
+    static constexpr int smem(bool copies) {
+        return K * (PAIR + BC) * 4 + 2 * K * 2 * S * 32 * 4 + (copies ? K * kStages * RAW : 0);
+    }
+};
+
+// Lane = state slice * CPW + channel; a lane holds states [ns * S, ns * S + S) of
+// its channel. A lane owns the kSlice / LN tokens of its channel (one, shared by
+// LN / kSlice lanes, where LN > kSlice) whose read-out it ends up with: it
+// prepares their inputs and stores their outputs.
+// kCopy: all rows allow the asynchronous copies of ScanShape; else element loads.
+template <typename T, int S, int LN, int K, bool kSeq, bool kCopy>
 __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(const SelectiveArgs a,
                                                                                 int units_per_group) {
-    constexpr int CPW = 32 / LN, NP = S * LN, S2 = S / 2;
-    constexpr int TPL = LN < kSlice ? kSlice / LN : 1;       // tokens owned by a lane
-    constexpr int SHARE = LN > kSlice ? LN / kSlice : 1;     // lanes that own the same token
-    constexpr int VEC = 16 / (int)sizeof(T);                 // B, C elements per 16-byte load
-    constexpr int NV = kSlice * 2 * NP / VEC / 32;           // such loads per lane and slice
-    constexpr bool kAhead = NV >= 1 && NV <= 2;              // load a tile ahead, in registers
+    using Sh = ScanShape<T, S, LN, K>;
+    constexpr int CPW = Sh::CPW, NP = Sh::NP, S2 = S / 2, S4 = S / 4, TPL = Sh::TPL;
+    constexpr int PROW = kSlice * 4 + 4;
     extern __shared__ float4 smem4[];
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int ch = lane % CPW, ns = lane / CPW, N = a.dstate;
-    float* sm_pair = reinterpret_cast<float*>(smem4) + w * (CPW * kPairStride);
-    float* sm_bc = reinterpret_cast<float*>(smem4) + K * (CPW * kPairStride) + w * (kSlice * 2 * NP);
-    // [2 buffers][K][E, P][S / 4][32] float4
-    float4* sm_ep = smem4 + K * (CPW * kPairStride + kSlice * 2 * NP) / 4;
+    float* sm_pair = reinterpret_cast<float*>(smem4) + w * Sh::PAIR;
+    float* sm_bc = reinterpret_cast<float*>(smem4) + K * Sh::PAIR + w * Sh::BC;
+    float4* sm_ep = smem4 + K * (Sh::PAIR + Sh::BC) / 4;  // [2 buffers][K][E, P][S / 4][32]
+    char* sm_raw = reinterpret_cast<char*>(sm_ep + 2 * K * 2 * S4 * 32) + w * (kStages * Sh::RAW);
 
     const int per = a.channels / a.ngroups;
     const int unit = blockIdx.x % units_per_group, bg = blockIdx.x / units_per_group;
@@ -85,10 +127,10 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
     const int c = g * per + (live ? unit * CPW + ch : per - 1);
     const int64_t row0 = (int64_t)b * a.seqlen;
     const int own = ns * kSlice / LN;  // first token of the slice that this lane owns
-    const bool owner = live && ns % SHARE == 0;
-    const T* u = static_cast<const T*>(a.u) + b * a.us_b + c;
-    const T* dt = static_cast<const T*>(a.dt) + b * a.ds_b + c;
-    const T* z = static_cast<const T*>(a.z) + b * a.zs_b + c;
+    const bool owner = live && ns % Sh::SHARE == 0;
+    const T* u = static_cast<const T*>(a.u) + b * a.us_b;
+    const T* dt = static_cast<const T*>(a.dt) + b * a.ds_b;
+    const T* z = static_cast<const T*>(a.z) + b * a.zs_b;
     const T* B = static_cast<const T*>(a.B) + b * a.bs_b + g * N;
     const T* C = static_cast<const T*>(a.C) + b * a.cs_b + g * N;
     T* y = static_cast<T*>(a.y) + row0 * a.channels + c;
@@ -112,7 +154,7 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
         }
     };
     const auto write_state = [&](const float2(&h)[S2], int s) {
-        if (!a.final_states || !live) return;
+        if (!live) return;
 #pragma unroll
         for (int j = 0; j < S2; ++j) {
             const int n = ns * S + 2 * j;
@@ -129,87 +171,126 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
         }
     };
 
-    // the lane's raw inputs of one slice
-    T ru[TPL], rd[TPL], rz[TPL];
-    const auto load_tokens = [&](int tw) {
+    // ---- inputs, ahead of their use: copies into shared memory, or registers ----
+    const T* tsrc[kCopy ? Sh::TR : 1];
+    int64_t tstep[kCopy ? Sh::TR : 1];
+    int tbytes[kCopy ? Sh::TR : 1];
+    const T* bsrc[kCopy ? Sh::BR : 1];
+    int64_t bstep[kCopy ? Sh::BR : 1];
+    T ru[kCopy ? 1 : TPL], rd[kCopy ? 1 : TPL], rz[kCopy ? 1 : TPL];
+    if constexpr (kCopy) {
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) {
-            const int t = tw + own + i;
-            ru[i] = rd[i] = rz[i] = from_f32<T>(0.f);
-            if (t < a.seqlen) {
-                ru[i] = u[t * a.us_t];
-                rd[i] = dt[t * a.ds_t];
-                if (a.z) rz[i] = z[t * a.zs_t];
-            }
+        for (int i = 0; i < Sh::TR; ++i) {  // copy v: array (u, dt, z), token, part of the token's channels
+            constexpr int PT = Sh::ROW / Sh::TB;
+            const int v = lane + 32 * i, arr = v / (kSlice * PT), tok = v / PT % kSlice, part = v % PT;
+            const int cg = unit * CPW + part * (Sh::TB / Sh::E);
+            const int64_t step = arr == 0 ? a.us_t : arr == 1 ? a.ds_t : a.zs_t;
+            tstep[i] = step * (K * kSlice);
+            tsrc[i] = (arr == 0 ? u : arr == 1 ? dt : z) + (w * kSlice + tok) * step + (g * per + min(cg, per - 1));
+            tbytes[i] = min(Sh::TB, max(0, per - cg) * Sh::E);
+            if (arr == 2 && !a.z) tbytes[i] = 0, tsrc[i] = u;  // no gate: zeros
+            if (arr > 2) tbytes[i] = -1;
         }
-    };
-    uint4 rbc[kAhead ? NV : 1];
-    // vector i of the slice's B and C: token, which of the two, first state
-    const auto bc_vector = [&](int tw, int i) {
-        constexpr int PT = NV >= 1 ? 2 * NP / VEC : 1;  // vectors per token
-        const int v = lane + 32 * i, tok = v / PT, r = v % PT, n = (r % (PT / 2 > 0 ? PT / 2 : 1)) * VEC;
-        const int t = tw + tok;
-        uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-        if (n < N && t < a.seqlen)
-            raw = *reinterpret_cast<const uint4*>((r < PT / 2 ? B + t * a.bs_t : C + t * a.cs_t) + n);
-        return raw;
-    };
-    const auto put_bc = [&](const uint4& raw, int i) {  // vectors lie in shared memory in their order
-        const T* e = reinterpret_cast<const T*>(&raw);
-        float* dst = sm_bc + (lane + 32 * i) * VEC;
 #pragma unroll
-        for (int k = 0; k < VEC; k += 4)
-            *reinterpret_cast<float4*>(dst + k) =
-                make_float4(to_f32(e[k]), to_f32(e[k + 1]), to_f32(e[k + 2]), to_f32(e[k + 3]));
-    };
-    const auto load_bc = [&](int tw) {
-        if constexpr (kAhead) {
-            if (a.bc_vectors) {
+        for (int i = 0; i < Sh::BR; ++i) {  // copy v: token, B or C, states
+            constexpr int PT = 2 * NP / Sh::BV;
+            const int v = lane + 32 * i, tok = v / PT, r = v % PT, n = r % (PT / 2) * Sh::BV;
+            const int64_t step = r < PT / 2 ? a.bs_t : a.cs_t;
+            bstep[i] = n < N ? step * (K * kSlice) : -1;
+            bsrc[i] = (r < PT / 2 ? B : C) + (w * kSlice + tok) * step + (n < N ? n : 0);
+        }
+    }
+    const auto fetch = [&](int tw, int stage) {  // the slice that starts at token tw
+        if constexpr (kCopy) {
+            char* dst = sm_raw + stage * Sh::RAW;
 #pragma unroll
-                for (int i = 0; i < NV; ++i) rbc[i] = bc_vector(tw, i);
+            for (int i = 0; i < Sh::TR; ++i) {
+                const int v = lane + 32 * i, tok = v / (Sh::ROW / Sh::TB) % kSlice;
+                if (tbytes[i] >= 0) {
+                    const bool in = tw + tok < a.seqlen;
+                    copy_async<Sh::TB>(dst + v * Sh::TB, in ? tsrc[i] : u, in ? tbytes[i] : 0);
+                    tsrc[i] += tstep[i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < Sh::BR; ++i) {
+                const int v = lane + 32 * i, tok = v / (2 * NP / Sh::BV);
+                const bool in = tw + tok < a.seqlen && bstep[i] >= 0;
+                copy_async<16>(dst + 3 * kSlice * Sh::ROW + v * 16, in ? bsrc[i] : B, in ? 16 : 0);
+                bsrc[i] += bstep[i];
+            }
+            copy_commit();
+        } else {
+#pragma unroll
+            for (int i = 0; i < TPL; ++i) {
+                const int t = tw + own + i;
+                ru[i] = rd[i] = rz[i] = from_f32<T>(0.f);
+                if (t < a.seqlen) {
+                    ru[i] = u[t * a.us_t + c];
+                    rd[i] = dt[t * a.ds_t + c];
+                    if (a.z) rz[i] = z[t * a.zs_t + c];
+                }
             }
         }
     };
 
     float2 h0[S2];  // the state before the tile, the same in every warp
-    init_state(h0, 0);
     if (kSeq) {
 #pragma unroll
         for (int j = 0; j < S2; ++j) h0[j] = both(0.f);
+    } else {
+        init_state(h0, 0);
     }
-    load_tokens(w * kSlice);
-    load_bc(w * kSlice);
-    int buf = 0;
+    fetch(w * kSlice, 0);
+    if (kCopy) fetch((K + w) * kSlice, 1);
+    int buf = 0, stage = 0;
     for (int t0 = 0; t0 < a.seqlen; t0 += K * kSlice, buf ^= 1) {
         const int tw = t0 + w * kSlice;
-        // ---- this slice's inputs: (delta, delta u), B, C to shared memory ----
+        // ---- this slice's (delta, delta u), B and C, in fp32 ----
+        if (kCopy) copy_wait<1>();
         __syncwarp();
+        const char* raw = sm_raw + stage * Sh::RAW;
         float skip[TPL], gate[TPL];
 #pragma unroll
         for (int i = 0; i < TPL; ++i) {
-            const float uf = to_f32(ru[i]);
-            float d = to_f32(rd[i]) + bias;
+            float uf, d, zf;
+            if constexpr (kCopy) {
+                const T* e = reinterpret_cast<const T*>(raw) + (own + i) * CPW + ch;
+                uf = to_f32(e[0]), d = to_f32(e[kSlice * CPW]), zf = to_f32(e[2 * kSlice * CPW]);
+            } else {
+                uf = to_f32(ru[i]), d = to_f32(rd[i]), zf = to_f32(rz[i]);
+            }
+            d += bias;
             if (a.softplus) d = softplus(d);
             if (tw + own + i >= a.seqlen) d = 0.f;  // past the end: a = 1 and no input
             skip[i] = D * uf;
-            gate[i] = a.z ? silu_for<T>(to_f32(rz[i])) : 1.f;
-            *reinterpret_cast<float2*>(sm_pair + ch * kPairStride + 2 * (own + i)) = make_float2(d, d * uf);
+            gate[i] = a.z ? silu_for<T>(zf) : 1.f;
+            const float du = d * uf;
+            *reinterpret_cast<float4*>(sm_pair + ch * PROW + 4 * (own + i)) = make_float4(d, d, du, du);
         }
-        bool staged = false;
-        if constexpr (NV >= 1) {
-            if (a.bc_vectors) {
-                staged = true;
+        if constexpr (kCopy) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) put_bc(kAhead ? rbc[kAhead ? i : 0] : bc_vector(tw, i), i);
+            for (int i = 0; i < Sh::BR; ++i) {
+                const int v = lane + 32 * i;
+                const Pack<T, Sh::BV> e = *reinterpret_cast<const Pack<T, Sh::BV>*>(raw + 3 * kSlice * Sh::ROW + v * 16);
+#pragma unroll
+                for (int k = 0; k < Sh::BV; k += 4)
+                    *reinterpret_cast<float4*>(sm_bc + v * Sh::BV + k) = make_float4(
+                        to_f32(e.v[k]), to_f32(e.v[k + 1]), to_f32(e.v[k + 2]), to_f32(e.v[k + 3]));
             }
-        }
-        if (!staged) {
-            for (int i = lane; i < kSlice * 2 * NP; i += 32) {
+        } else {
+            for (int i = lane; i < Sh::BC; i += 32) {
                 const int tok = i / (2 * NP), r = i % (2 * NP), n = r % NP, t = tw + tok;
                 float v = 0.f;
                 if (n < N && t < a.seqlen) v = to_f32(r < NP ? B[t * a.bs_t + n] : C[t * a.cs_t + n]);
                 sm_bc[i] = v;
             }
+        }
+        if (kCopy) {
+            fetch(tw + 2 * K * kSlice, stage == 0 ? 2 : stage - 1);
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+        } else {
+            fetch(tw + K * kSlice, 0);
         }
         // sequences that start in this slice: lane i < kSlice looks at token tw + i
         unsigned starts = 0u;
@@ -221,35 +302,38 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
             starts = __ballot_sync(0xffffffffu, lane < kSlice && tw + lane < a.seqlen && (t == 0 || id != id_before));
         }
         __syncwarp();
-        load_tokens(tw + K * kSlice);
-        load_bc(tw + K * kSlice);
-        // ---- the slice from zero: a (kept), end state E, product P ----
-        float2 av[kSlice][S2], E[S2], P[S2];
+        // ---- the slice from zero: local state l, decay p, C l, and C p (kept) ----
+        float2 l[S2], p[S2], cp[kSlice][S2], acc[kSlice];
 #pragma unroll
-        for (int j = 0; j < S2; ++j) E[j] = both(0.f), P[j] = both(1.f);
+        for (int j = 0; j < S2; ++j) l[j] = both(0.f), p[j] = both(1.f);
 #pragma unroll
         for (int t = 0; t < kSlice; ++t) {
-            const float2 dd = *reinterpret_cast<const float2*>(sm_pair + ch * kPairStride + 2 * t);
-            const float2* Bt = reinterpret_cast<const float2*>(sm_bc + t * 2 * NP + ns * S);
+            const float4 dd = *reinterpret_cast<const float4*>(sm_pair + ch * PROW + 4 * t);
+            const float4* Bt = reinterpret_cast<const float4*>(sm_bc + t * 2 * NP + ns * S);
+            const float4* Ct = reinterpret_cast<const float4*>(sm_bc + t * 2 * NP + NP + ns * S);
             if (kSeq && (starts >> t & 1u)) {
-                init_state(E, __shfl_sync(0xffffffffu, id, t));
+                init_state(l, __shfl_sync(0xffffffffu, id, t));
 #pragma unroll
-                for (int j = 0; j < S2; ++j) P[j] = both(0.f);
+                for (int j = 0; j < S2; ++j) p[j] = both(0.f);
             }
+            acc[t] = both(0.f);
 #pragma unroll
             for (int j = 0; j < S2; ++j) {
-                const float2 x = __fmul2_rn(both(dd.x), A2[j]);
-                av[t][j] = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                E[j] = __ffma2_rn(av[t][j], E[j], __fmul2_rn(both(dd.y), Bt[j]));
-                P[j] = __fmul2_rn(P[j], av[t][j]);
+                const float2 x = __fmul2_rn(lo2(dd), A2[j]);
+                const float2 av = make_float2(exp2_fast(x.x), exp2_fast(x.y));
+                const float2 Bj = j % 2 ? hi2(Bt[j / 2]) : lo2(Bt[j / 2]), Cj = j % 2 ? hi2(Ct[j / 2]) : lo2(Ct[j / 2]);
+                l[j] = __ffma2_rn(av, l[j], __fmul2_rn(hi2(dd), Bj));
+                p[j] = __fmul2_rn(p[j], av);
+                acc[t] = __ffma2_rn(Cj, l[j], acc[t]);
+                cp[t][j] = __fmul2_rn(Cj, p[j]);
             }
         }
         // ---- chain the slices: the state before this one, and before the next tile ----
-        float4* ep = sm_ep + (buf * K * 2) * (S / 4) * 32 + lane;
+        float4* ep = sm_ep + (buf * K * 2) * S4 * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < S / 4; ++j) {
-            ep[((w * 2 + 0) * (S / 4) + j) * 32] = make_float4(E[2 * j].x, E[2 * j].y, E[2 * j + 1].x, E[2 * j + 1].y);
-            ep[((w * 2 + 1) * (S / 4) + j) * 32] = make_float4(P[2 * j].x, P[2 * j].y, P[2 * j + 1].x, P[2 * j + 1].y);
+        for (int j = 0; j < S4; ++j) {
+            ep[((w * 2 + 0) * S4 + j) * 32] = make_float4(l[2 * j].x, l[2 * j].y, l[2 * j + 1].x, l[2 * j + 1].y);
+            ep[((w * 2 + 1) * S4 + j) * 32] = make_float4(p[2 * j].x, p[2 * j].y, p[2 * j + 1].x, p[2 * j + 1].y);
         }
         __syncthreads();
         float2 h[S2];
@@ -260,37 +344,47 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
                 for (int j = 0; j < S2; ++j) h[j] = h0[j];
             }
 #pragma unroll
-            for (int j = 0; j < S / 4; ++j) {
-                const float4 e = ep[((k * 2 + 0) * (S / 4) + j) * 32], p = ep[((k * 2 + 1) * (S / 4) + j) * 32];
-                h0[2 * j] = __ffma2_rn(make_float2(p.x, p.y), h0[2 * j], make_float2(e.x, e.y));
-                h0[2 * j + 1] = __ffma2_rn(make_float2(p.z, p.w), h0[2 * j + 1], make_float2(e.z, e.w));
+            for (int j = 0; j < S4; ++j) {
+                const float4 e = ep[((k * 2 + 0) * S4 + j) * 32], q = ep[((k * 2 + 1) * S4 + j) * 32];
+                h0[2 * j] = __ffma2_rn(lo2(q), h0[2 * j], lo2(e));
+                h0[2 * j + 1] = __ffma2_rn(hi2(q), h0[2 * j + 1], hi2(e));
             }
         }
-        // ---- the slice from its true state, and the read-out ----
-        float acc[kSlice];
+        // ---- the read-out of the state before the slice ----
+        float out[kSlice];
 #pragma unroll
         for (int t = 0; t < kSlice; ++t) {
-            const float du = sm_pair[ch * kPairStride + 2 * t + 1];
-            const float2* Bt = reinterpret_cast<const float2*>(sm_bc + t * 2 * NP + ns * S);
-            const float2* Ct = reinterpret_cast<const float2*>(sm_bc + t * 2 * NP + NP + ns * S);
-            if (kSeq && (starts >> t & 1u)) {
-                const int s = __shfl_sync(0xffffffffu, id, t), p = __shfl_sync(0xffffffffu, id_before, t);
-                if (p >= 0) write_state(h, p);
-                keep(p + 1, s);
-                init_state(h, s);
-            }
-            float2 r = both(0.f);
 #pragma unroll
-            for (int j = 0; j < S2; ++j) {
-                h[j] = __ffma2_rn(av[t][j], h[j], __fmul2_rn(both(du), Bt[j]));
-                r = __ffma2_rn(Ct[j], h[j], r);
-            }
-            acc[t] = r.x + r.y;
+            for (int j = 0; j < S2; ++j) acc[t] = __ffma2_rn(cp[t][j], h[j], acc[t]);
+            out[t] = acc[t].x + acc[t].y;
         }
-        if (a.final_states && tw < a.seqlen && tw + kSlice >= a.seqlen) {  // this slice has the last token
-            const int s = kSeq ? __shfl_sync(0xffffffffu, id, a.seqlen - 1 - tw) : 0;
-            write_state(h, s);
-            keep(s + 1, a.nseq);
+        // ---- final states: of sequences that end inside the slice, and of the row's last ----
+        if (a.final_states) {
+            const bool last = tw < a.seqlen && tw + kSlice >= a.seqlen;
+            if (last) {
+#pragma unroll
+                for (int j = 0; j < S2; ++j) l[j] = __ffma2_rn(p[j], h[j], l[j]);
+                const int s = kSeq ? __shfl_sync(0xffffffffu, id, a.seqlen - 1 - tw) : 0;
+                write_state(l, s);
+                keep(s + 1, a.nseq);
+            }
+            if (kSeq && starts) {  // rare: walk the slice again from its true state
+                for (int t = 0; t < kSlice; ++t) {
+                    if (starts >> t & 1u) {
+                        const int s = __shfl_sync(0xffffffffu, id, t), before = __shfl_sync(0xffffffffu, id_before, t);
+                        if (before >= 0) write_state(h, before);
+                        keep(before + 1, s);
+                        init_state(h, s);
+                    }
+                    const float4 dd = *reinterpret_cast<const float4*>(sm_pair + ch * PROW + 4 * t);
+#pragma unroll
+                    for (int j = 0; j < S2; ++j) {
+                        const float2 Bj = *reinterpret_cast<const float2*>(sm_bc + t * 2 * NP + ns * S + 2 * j);
+                        const float2 x = __fmul2_rn(lo2(dd), A2[j]);
+                        h[j] = __ffma2_rn(make_float2(exp2_fast(x.x), exp2_fast(x.y)), h[j], __fmul2_rn(hi2(dd), Bj));
+                    }
+                }
+            }
         }
         // ---- sum over the channel's lanes; each ends with the tokens it owns ----
 #pragma unroll
@@ -300,18 +394,18 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
                 const bool up = ns & m;
 #pragma unroll
                 for (int i = 0; i < n; ++i) {
-                    const float give = up ? acc[i] : acc[i + n], stay = up ? acc[i + n] : acc[i];
-                    acc[i] = stay + __shfl_xor_sync(0xffffffffu, give, m * CPW);
+                    const float give = up ? out[i] : out[i + n], stay = up ? out[i + n] : out[i];
+                    out[i] = stay + __shfl_xor_sync(0xffffffffu, give, m * CPW);
                 }
             } else {
-                acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], m * CPW);
+                out[0] += __shfl_xor_sync(0xffffffffu, out[0], m * CPW);
             }
         }
         if (owner) {
 #pragma unroll
             for (int i = 0; i < TPL; ++i) {
                 const int t = tw + own + i;
-                if (t < a.seqlen) y[(int64_t)t * a.channels] = from_f32<T>((acc[i] + skip[i]) * gate[i]);
+                if (t < a.seqlen) y[(int64_t)t * a.channels] = from_f32<T>((out[i] + skip[i]) * gate[i]);
             }
         }
     }
@@ -353,14 +447,14 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Sele
     static_cast<T*>(a.y)[(int64_t)b * a.channels + c] = from_f32<T>(y);
 }
 
-template <typename T, int S, int LN, int K>
-cudaError_t run_scan(const SelectiveArgs& a, cudaStream_t st) {
-    constexpr int CPW = 32 / LN, NP = S * LN;
-    constexpr int smem = (K * (CPW * kPairStride + kSlice * 2 * NP) + 2 * K * 2 * S * 32) * (int)sizeof(float);
+template <typename T, int S, int LN, int K, bool kSeq, bool kCopy>
+cudaError_t start_scan(const SelectiveArgs& a, cudaStream_t st) {
+    using Sh = ScanShape<T, S, LN, K>;
+    constexpr int smem = Sh::smem(kCopy);
     static_assert(smem <= 227 * 1024, "fits one SM");
-    const int per = a.channels / a.ngroups, units = (per + CPW - 1) / CPW;
+    const int per = a.channels / a.ngroups, units = (per + Sh::CPW - 1) / Sh::CPW;
     const unsigned grid = (unsigned)((int64_t)a.batch * a.ngroups * units);
-    const auto kernel = a.seq_idx ? selective_scan_kernel<T, S, LN, K, true> : selective_scan_kernel<T, S, LN, K, false>;
+    const auto kernel = selective_scan_kernel<T, S, LN, K, kSeq, kCopy>;
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -370,21 +464,34 @@ cudaError_t run_scan(const SelectiveArgs& a, cudaStream_t st) {
     return cudaGetLastError();
 }
 
+template <typename T, int S, int LN, int K>
+cudaError_t run_scan(const SelectiveArgs& a, cudaStream_t st) {
+    using Sh = ScanShape<T, S, LN, K>;
+    if constexpr (Sh::kCanCopy) {
+        VectorRule tok(sizeof(T)), bc(sizeof(T));
+        tok.address(a.u).address(a.dt).elements(a.us_b).elements(a.us_t).elements(a.ds_b).elements(a.ds_t);
+        if (a.z) tok.address(a.z).elements(a.zs_b).elements(a.zs_t);
+        tok.elements(a.channels / a.ngroups);
+        bc.address(a.B).address(a.C).elements(a.bs_b).elements(a.bs_t).elements(a.cs_b).elements(a.cs_t);
+        bc.elements(a.dstate);
+        if (tok.multiple_of(Sh::TB) && bc.multiple_of(16))
+            return a.seq_idx ? start_scan<T, S, LN, K, true, true>(a, st) : start_scan<T, S, LN, K, false, true>(a, st);
+    }
+    return a.seq_idx ? start_scan<T, S, LN, K, true, false>(a, st) : start_scan<T, S, LN, K, false, false>(a, st);
+}
+
 template <typename T, int S, int LN>
 cudaError_t scan_by_slices(const SelectiveArgs& a, cudaStream_t st) {
     const int64_t units = (int64_t)a.batch * a.ngroups * ((a.channels / a.ngroups + 32 / LN - 1) / (32 / LN));
     // 16 warps per CTA where the CTAs do not fill the GPU's SMs twice, else 4
-    if constexpr (S * LN <= 128) {
+    if constexpr (S * LN <= 64) {
         if (units < 2 * 148 && a.seqlen > 4 * kSlice) return run_scan<T, S, LN, 16>(a, st);
     }
     return run_scan<T, S, LN, 4>(a, st);
 }
 
 template <typename T>
-cudaError_t scan_by_states(SelectiveArgs a, cudaStream_t st) {
-    VectorRule r(sizeof(T));
-    r.address(a.B).address(a.C).elements(a.bs_b).elements(a.bs_t).elements(a.cs_b).elements(a.cs_t).elements(a.dstate);
-    a.bc_vectors = r.multiple_of(16);
+cudaError_t scan_by_states(const SelectiveArgs& a, cudaStream_t st) {
     if (a.dstate <= 8) return scan_by_slices<T, 4, 2>(a, st);
     if (a.dstate <= 16) return scan_by_slices<T, 4, 4>(a, st);
     if (a.dstate <= 32) return scan_by_slices<T, 4, 8>(a, st);
