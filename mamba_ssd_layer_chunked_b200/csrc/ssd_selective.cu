@@ -9,18 +9,16 @@
 // chunked matrix form of the scalar-decay scan does not exist here: the work is
 // one exponential and three multiply-adds per (token, channel, state).
 //
-// Prompts: a warp owns a few channels of one row, LN lanes per channel with S
-// states each in registers, and a CTA's K warps take consecutive slices of
-// kSlice tokens, so that the exponentials of K * kSlice tokens are formed at
-// once although the recurrence is sequential. Over a slice the recurrence is
-// affine in the state before it: with the local state (from zero) l_t and the
-// decay p_t since the slice's start, h_t = l_t + p_t h_start, so
-//   y_t = C_t . l_t + (C_t p_t) . h_start.
-// Each warp walks its slice once, keeping C_t p_t in registers, the warps
-// exchange (l_end, p_end) once per tile through shared memory, each chains the
-// slices before its own, and adds the second term. Every exponential is formed
-// once. Bound by the special-function unit (one exponential per (token,
-// channel, state)) and the issue rate together.
+// Prompts: a warp owns a few channels of one row, LN lanes per CH channels with
+// S states of each in registers. The exponentials do not depend on the state, so
+// a CTA's K warps take consecutive slices of L tokens in turn: each forms
+// a = exp(delta A) and v = delta u B of its slice in registers, waits for the
+// state that the warp before it leaves in shared memory (a named barrier between
+// the two), runs the L dependent multiply-adds, hands the state on, and reads
+// out. The chain is short beside the rest, so the warps work side by side
+// although the recurrence is sequential. Every exponential is formed once.
+// Bound by the special-function unit (one exponential per (token, channel,
+// state)) and by shared memory's B, C and delta, read once per lane.
 
 #include "ssd_block.cuh"
 
@@ -29,7 +27,6 @@ namespace ssd {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kSlice = 8;       // tokens per warp and tile
 
 // 2^x, the hardware approximation (denormal results flushed to 0)
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -56,10 +53,6 @@ __device__ __forceinline__ float softplus(float z) {
     return fmaf(2.f * r, s, fmaxf(z, 0.f));
 }
 
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 lo2(const float4& v) { return make_float2(v.x, v.y); }
-__device__ __forceinline__ float2 hi2(const float4& v) { return make_float2(v.z, v.w); }
-
 // Asynchronous copy of `bytes` bytes (2, 4, ... kBytes) to shared memory, zeros behind them.
 template <int kBytes>
 __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
@@ -78,97 +71,131 @@ __device__ __forceinline__ void copy_wait() {
 
 constexpr int kStages = 3;  // slices of raw inputs in shared memory: two in flight behind the current one
 
-// Layout of the scan's shared memory and its copies, for S states per lane, LN
-// lanes per channel, K warps.
-template <typename T, int S, int LN, int K>
+// CH channels and S states of each per lane, LN lanes per channel, slices of L
+// tokens, K warps.
+template <typename T, int CH_, int S_, int LN_, int L_, int K_>
 struct ScanShape {
-    static constexpr int CPW = 32 / LN;                                // channels per warp
-    static constexpr int NP = S * LN;                                  // states, padded
+    static constexpr int CH = CH_, S = S_, LN = LN_, L = L_, K = K_;
+    static constexpr int COLS = 32 / LN;                       // lanes side by side in channels
+    static constexpr int CPW = COLS * CH;                      // channels per warp
+    static constexpr int NP = S * LN;                          // states, padded
     static constexpr int E = (int)sizeof(T);
-    static constexpr int TPL = LN < kSlice ? kSlice / LN : 1;          // tokens owned by a lane
-    static constexpr int SHARE = LN > kSlice ? LN / kSlice : 1;        // lanes that own the same token
-    static constexpr int ROW = CPW * E;                                // bytes of a token's channels
-    static constexpr int TB = ROW < 16 ? ROW : 16;                     // bytes per copy of u, dt, z
-    static constexpr int TR = (3 * kSlice * ROW / TB + 31) / 32;       // such copies per lane and slice
-    static constexpr int BV = 16 / E;                                  // B, C elements per copy
-    static constexpr int BR = kSlice * 2 * NP / BV / 32;               // such copies per lane and slice
-    static constexpr bool kCanCopy = TB >= 4 && NP >= BV && BR >= 1 && BR <= 4;
-    static constexpr int PAIR = CPW * (kSlice * 4 + 4);                // floats: (delta, delta, du, du) per token
-    static constexpr int BC = kSlice * 2 * NP;                         // floats: B and C of the slice
-    static constexpr int RAW = 3 * kSlice * ROW + BC * E;              // bytes of a raw stage
-    static constexpr int smem(bool copies) {
-        return K * (PAIR + BC) * 4 + 2 * K * 2 * S * 32 * 4 + (copies ? K * kStages * RAW : 0);
-    }
+    static constexpr int OUTS = CH * L;                        // (token, channel) sums a lane takes part in
+    static constexpr int OWN = LN < OUTS ? OUTS / LN : 1;      // of those, the ones it ends up with
+    static constexpr int SHARE = LN > OUTS ? LN / OUTS : 1;    // lanes that end up with the same one
+    static constexpr int ROW = CPW * E;                        // bytes of a token's channels
+    static constexpr int TB = ROW < 16 ? ROW : 16;             // bytes per copy of u, dt, z
+    static constexpr int TR = (3 * L * ROW / TB + 31) / 32;    // such copies per lane and slice
+    static constexpr int BV = 16 / E;                          // B, C elements per copy
+    static constexpr int BN = L * 2 * NP / BV;                 // such copies per slice
+    static constexpr int BR = (BN + 31) / 32;                  // and per lane
+    static constexpr bool kCanCopy = TB >= 4 && NP >= BV && BR <= 4;
+    static constexpr int VW = CH == 2 && OWN % 2 == 0 ? 2 : 1; // owned channels that lie side by side
+    static constexpr int PAIR = L * CPW * 2;                   // floats: (delta, delta u) per token and channel
+    static constexpr int BC = L * 2 * NP;                      // floats: B and C of the slice
+    static constexpr int STATE = CH * S * 32;                  // floats: a state handed on
+    static constexpr int RAW = 3 * L * ROW + BC * E;           // bytes of a raw stage
+    static constexpr int smem(bool copies) { return K * (PAIR + BC + STATE) * 4 + (copies ? K * kStages * RAW : 0); }
 };
 
-// Lane = state slice * CPW + channel; a lane holds states [ns * S, ns * S + S) of
-// its channel. A lane owns the kSlice / LN tokens of its channel (one, shared by
-// LN / kSlice lanes, where LN > kSlice) whose read-out it ends up with: it
-// prepares their inputs and stores their outputs.
-// kCopy: all rows allow the asynchronous copies of ScanShape; else element loads.
-template <typename T, int S, int LN, int K, bool kSeq, bool kCopy>
-__global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(const SelectiveArgs a,
-                                                                                int units_per_group) {
-    using Sh = ScanShape<T, S, LN, K>;
-    constexpr int CPW = Sh::CPW, NP = Sh::NP, S2 = S / 2, S4 = S / 4, TPL = Sh::TPL;
-    constexpr int PROW = kSlice * 4 + 4;
+// Lane = state slice * COLS + column; a lane holds states [ns * S, ns * S + S) of
+// the CH channels of its column. Of the OUTS sums over states that the LN lanes of
+// a column form together (token-major, its CH channels within a token) a lane
+// ends up with OWN; those (token, channel) are also the ones whose inputs it
+// prepares. kCopy: all rows allow the asynchronous copies of ScanShape.
+template <typename T, typename Sh, int kMinCtas, bool kSeq, bool kCopy>
+__global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(const SelectiveArgs a,
+                                                                              int units_per_group) {
+    constexpr int CH = Sh::CH, S = Sh::S, L = Sh::L, K = Sh::K, COLS = Sh::COLS, CPW = Sh::CPW, NP = Sh::NP;
+    constexpr int S2 = S / 2, OWN = Sh::OWN, VW = Sh::VW;
     extern __shared__ float4 smem4[];
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int ch = lane % CPW, ns = lane / CPW, N = a.dstate;
-    float* sm_pair = reinterpret_cast<float*>(smem4) + w * Sh::PAIR;
-    float* sm_bc = reinterpret_cast<float*>(smem4) + K * Sh::PAIR + w * Sh::BC;
-    float4* sm_ep = smem4 + K * (Sh::PAIR + Sh::BC) / 4;  // [2 buffers][K][E, P][S / 4][32]
-    char* sm_raw = reinterpret_cast<char*>(sm_ep + 2 * K * 2 * S4 * 32) + w * (kStages * Sh::RAW);
+    const int col = lane % COLS, ns = lane / COLS, N = a.dstate;
+    constexpr int kWarpBytes = (Sh::PAIR + Sh::BC + Sh::STATE) * 4 + (kCopy ? kStages * Sh::RAW : 0);
+    char* mine4 = reinterpret_cast<char*>(smem4) + w * kWarpBytes;  // the warp's part
+    float* sm_pair = reinterpret_cast<float*>(mine4);
+    float* sm_bc = sm_pair + Sh::PAIR;
+    float4* sm_state = reinterpret_cast<float4*>(sm_bc + Sh::BC) + lane;  // [CH * S / 4][32]
+    float4* sm_next = reinterpret_cast<float4*>(
+        reinterpret_cast<char*>(sm_state) + (w == K - 1 ? -(K - 1) * kWarpBytes : kWarpBytes));
+    char* sm_raw = reinterpret_cast<char*>(sm_bc + Sh::BC + Sh::STATE);
 
     const int per = a.channels / a.ngroups;
     const int unit = blockIdx.x % units_per_group, bg = blockIdx.x / units_per_group;
     const int g = bg % a.ngroups, b = bg / a.ngroups;
-    const bool live = unit * CPW + ch < per;
-    const int c = g * per + (live ? unit * CPW + ch : per - 1);
+    const int cg0 = unit * CPW;  // the warp's first channel within the group
     const int64_t row0 = (int64_t)b * a.seqlen;
-    const int own = ns * kSlice / LN;  // first token of the slice that this lane owns
-    const bool owner = live && ns % Sh::SHARE == 0;
-    const T* u = static_cast<const T*>(a.u) + b * a.us_b;
-    const T* dt = static_cast<const T*>(a.dt) + b * a.ds_b;
-    const T* z = static_cast<const T*>(a.z) + b * a.zs_b;
+    const T* u = static_cast<const T*>(a.u) + b * a.us_b + g * per;
+    const T* dt = static_cast<const T*>(a.dt) + b * a.ds_b + g * per;
+    const T* z = static_cast<const T*>(a.z) + b * a.zs_b + g * per;
     const T* B = static_cast<const T*>(a.B) + b * a.bs_b + g * N;
     const T* C = static_cast<const T*>(a.C) + b * a.cs_b + g * N;
-    T* y = static_cast<T*>(a.y) + row0 * a.channels + c;
-    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f;
-    const float D = a.D ? a.D[c] : 0.f;
 
-    float2 A2[S2];
+    // the lane's own (token, channel) pairs: tok(i), and cg(i) within the group
+    const int first = ns * Sh::OUTS / Sh::LN;
+    const auto tok = [&](int i) { return (first + i) / CH; };
+    const auto cl = [&](int i) { return col * CH + (first + i) % CH; };  // within the warp's channels
+    float bias[OWN], D[OWN];
+    bool mine[OWN];
 #pragma unroll
-    for (int j = 0; j < S2; ++j) {
-        const int n = ns * S + 2 * j;
-        A2[j].x = n < N ? a.A[(int64_t)c * N + n] * kLog2e : 0.f;
-        A2[j].y = n + 1 < N ? a.A[(int64_t)c * N + n + 1] * kLog2e : 0.f;
+    for (int i = 0; i < OWN; ++i) {
+        const int cg = min(cg0 + cl(i), per - 1), c = g * per + cg;
+        mine[i] = cg0 + cl(i) < per && ns % Sh::SHARE == 0;
+        bias[i] = a.dt_bias ? a.dt_bias[c] : 0.f;
+        D[i] = a.D ? a.D[c] : 0.f;
     }
-    const auto state_at = [&](int s, int n) { return (((int64_t)b * a.nseq + s) * N + n) * a.channels + c; };
-    const auto init_state = [&](float2(&h)[S2], int s) {
+    // the lane's states: channel m, states ns * S + 2 j, + 1
+    float2 A2[CH][S2];
+#pragma unroll
+    for (int m = 0; m < CH; ++m)
 #pragma unroll
         for (int j = 0; j < S2; ++j) {
             const int n = ns * S + 2 * j;
-            h[j].x = a.init && n < N ? a.init[state_at(s, n)] : 0.f;
-            h[j].y = a.init && n + 1 < N ? a.init[state_at(s, n + 1)] : 0.f;
+            const int64_t r = (int64_t)(g * per + min(cg0 + col * CH + m, per - 1)) * N;
+            A2[m][j].x = n < N ? a.A[r + n] * kLog2e : 0.f;
+            A2[m][j].y = n + 1 < N ? a.A[r + n + 1] * kLog2e : 0.f;
+        }
+    using State = float2[CH][S2];
+    const auto each_state = [&](int s, const auto& f) {  // f(m, n's pair j, which of the two, offset)
+        for (int m = 0; m < CH; ++m) {
+            const int cg = cg0 + col * CH + m;
+            if (cg >= per) break;
+            for (int j = 0; j < S; ++j) {
+                const int n = ns * S + j;
+                if (n < N) f(m, j, (((int64_t)b * a.nseq + s) * N + n) * a.channels + g * per + cg);
+            }
         }
     };
-    const auto write_state = [&](const float2(&h)[S2], int s) {
-        if (!live) return;
+    const auto init_state = [&](State& h, int s) {
 #pragma unroll
-        for (int j = 0; j < S2; ++j) {
-            const int n = ns * S + 2 * j;
-            if (n < N) a.final_states[state_at(s, n)] = h[j].x;
-            if (n + 1 < N) a.final_states[state_at(s, n + 1)] = h[j].y;
+        for (int m = 0; m < CH; ++m) {
+            const int cg = min(cg0 + col * CH + m, per - 1);
+#pragma unroll
+            for (int j = 0; j < S2; ++j) {
+                const int n = ns * S + 2 * j;
+                const int64_t o = (((int64_t)b * a.nseq + s) * N + n) * a.channels + g * per + cg;
+                h[m][j].x = a.init && n < N ? a.init[o] : 0.f;
+                h[m][j].y = a.init && n + 1 < N ? a.init[o + a.channels] : 0.f;
+            }
+        }
+    };
+    const auto write_state = [&](const State& h, int s) {
+#pragma unroll
+        for (int m = 0; m < CH; ++m) {
+            const int cg = cg0 + col * CH + m;
+#pragma unroll
+            for (int j = 0; j < S2; ++j) {
+                const int n = ns * S + 2 * j;
+                const int64_t o = (((int64_t)b * a.nseq + s) * N + n) * a.channels + g * per + cg;
+                if (cg < per && n < N) a.final_states[o] = h[m][j].x;
+                if (cg < per && n + 1 < N) a.final_states[o + a.channels] = h[m][j].y;
+            }
         }
     };
     // ids that do not occur keep their initial state
     const auto keep = [&](int lo, int hi) {
-        for (int s = lo; s < hi; ++s) {
-            float2 h[S2];
-            init_state(h, s);
-            write_state(h, s);
-        }
+        for (int s = lo; s < hi; ++s)
+            each_state(s, [&](int, int, int64_t o) { a.final_states[o] = a.init ? a.init[o] : 0.f; });
     };
 
     // ---- inputs, ahead of their use: copies into shared memory, or registers ----
@@ -177,237 +204,251 @@ __global__ void __launch_bounds__(32 * K, K == 4 ? 5 : 1) selective_scan_kernel(
     int tbytes[kCopy ? Sh::TR : 1];
     const T* bsrc[kCopy ? Sh::BR : 1];
     int64_t bstep[kCopy ? Sh::BR : 1];
-    T ru[kCopy ? 1 : TPL], rd[kCopy ? 1 : TPL], rz[kCopy ? 1 : TPL];
+    T ru[kCopy ? 1 : OWN], rd[kCopy ? 1 : OWN], rz[kCopy ? 1 : OWN];
     if constexpr (kCopy) {
+        constexpr int PT = Sh::ROW / Sh::TB, PB = 2 * NP / Sh::BV;
 #pragma unroll
         for (int i = 0; i < Sh::TR; ++i) {  // copy v: array (u, dt, z), token, part of the token's channels
-            constexpr int PT = Sh::ROW / Sh::TB;
-            const int v = lane + 32 * i, arr = v / (kSlice * PT), tok = v / PT % kSlice, part = v % PT;
-            const int cg = unit * CPW + part * (Sh::TB / Sh::E);
+            const int v = lane + 32 * i, arr = v / (L * PT), t = v / PT % L, part = v % PT;
+            const int cg = cg0 + part * (Sh::TB / Sh::E);
             const int64_t step = arr == 0 ? a.us_t : arr == 1 ? a.ds_t : a.zs_t;
-            tstep[i] = step * (K * kSlice);
-            tsrc[i] = (arr == 0 ? u : arr == 1 ? dt : z) + (w * kSlice + tok) * step + (g * per + min(cg, per - 1));
+            tstep[i] = step * (K * L);
+            tsrc[i] = (arr == 0 ? u : arr == 1 ? dt : z) + (w * L + t) * step + min(cg, per - 1);
             tbytes[i] = min(Sh::TB, max(0, per - cg) * Sh::E);
-            if (arr == 2 && !a.z) tbytes[i] = 0, tsrc[i] = u;  // no gate: zeros
+            if (arr == 2 && !a.z) tbytes[i] = 0, tsrc[i] = u, tstep[i] = 0;  // no gate: zeros
             if (arr > 2) tbytes[i] = -1;
         }
 #pragma unroll
         for (int i = 0; i < Sh::BR; ++i) {  // copy v: token, B or C, states
-            constexpr int PT = 2 * NP / Sh::BV;
-            const int v = lane + 32 * i, tok = v / PT, r = v % PT, n = r % (PT / 2) * Sh::BV;
-            const int64_t step = r < PT / 2 ? a.bs_t : a.cs_t;
-            bstep[i] = n < N ? step * (K * kSlice) : -1;
-            bsrc[i] = (r < PT / 2 ? B : C) + (w * kSlice + tok) * step + (n < N ? n : 0);
+            const int v = lane + 32 * i, t = v / PB, r = v % PB, n = r % (PB / 2) * Sh::BV;
+            const int64_t step = r < PB / 2 ? a.bs_t : a.cs_t;
+            bstep[i] = n < N ? step * (K * L) : -1;
+            bsrc[i] = (r < PB / 2 ? B : C) + (w * L + t) * step + (n < N ? n : 0);
         }
     }
     const auto fetch = [&](int tw, int stage) {  // the slice that starts at token tw
         if constexpr (kCopy) {
-            char* dst = sm_raw + stage * Sh::RAW;
+            char* dst = sm_raw + stage + lane * Sh::TB;
+            char* dst_bc = sm_raw + stage + 3 * L * Sh::ROW + lane * 16;
+            const bool full = tw + L <= a.seqlen;
 #pragma unroll
             for (int i = 0; i < Sh::TR; ++i) {
-                const int v = lane + 32 * i, tok = v / (Sh::ROW / Sh::TB) % kSlice;
+                const int t = (lane + 32 * i) / (Sh::ROW / Sh::TB) % L;
                 if (tbytes[i] >= 0) {
-                    const bool in = tw + tok < a.seqlen;
-                    copy_async<Sh::TB>(dst + v * Sh::TB, in ? tsrc[i] : u, in ? tbytes[i] : 0);
+                    if (full)
+                        copy_async<Sh::TB>(dst + i * 32 * Sh::TB, tsrc[i], tbytes[i]);
+                    else
+                        copy_async<Sh::TB>(dst + i * 32 * Sh::TB, tw + t < a.seqlen ? tsrc[i] : u,
+                                           tw + t < a.seqlen ? tbytes[i] : 0);
                     tsrc[i] += tstep[i];
                 }
             }
 #pragma unroll
             for (int i = 0; i < Sh::BR; ++i) {
-                const int v = lane + 32 * i, tok = v / (2 * NP / Sh::BV);
-                const bool in = tw + tok < a.seqlen && bstep[i] >= 0;
-                copy_async<16>(dst + 3 * kSlice * Sh::ROW + v * 16, in ? bsrc[i] : B, in ? 16 : 0);
-                bsrc[i] += bstep[i];
+                const int t = (lane + 32 * i) / (2 * NP / Sh::BV);
+                if (Sh::BN % 32 == 0 || lane + 32 * i < Sh::BN) {
+                    const bool in = (full || tw + t < a.seqlen) && bstep[i] >= 0;
+                    copy_async<16>(dst_bc + i * 512, in ? bsrc[i] : B, in ? 16 : 0);
+                    bsrc[i] += bstep[i];
+                }
             }
             copy_commit();
         } else {
 #pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-                const int t = tw + own + i;
+            for (int i = 0; i < OWN; ++i) {
+                const int t = tw + tok(i), cg = min(cg0 + cl(i), per - 1);
                 ru[i] = rd[i] = rz[i] = from_f32<T>(0.f);
                 if (t < a.seqlen) {
-                    ru[i] = u[t * a.us_t + c];
-                    rd[i] = dt[t * a.ds_t + c];
-                    if (a.z) rz[i] = z[t * a.zs_t + c];
+                    ru[i] = u[t * a.us_t + cg];
+                    rd[i] = dt[t * a.ds_t + cg];
+                    if (a.z) rz[i] = z[t * a.zs_t + cg];
                 }
             }
         }
     };
 
-    float2 h0[S2];  // the state before the tile, the same in every warp
-    if (kSeq) {
-#pragma unroll
-        for (int j = 0; j < S2; ++j) h0[j] = both(0.f);
-    } else {
-        init_state(h0, 0);
-    }
-    fetch(w * kSlice, 0);
-    if (kCopy) fetch((K + w) * kSlice, 1);
-    int buf = 0, stage = 0;
-    for (int t0 = 0; t0 < a.seqlen; t0 += K * kSlice, buf ^= 1) {
-        const int tw = t0 + w * kSlice;
+    fetch(w * L, 0);
+    if (kCopy) fetch((K + w) * L, Sh::RAW);
+    int stage = 0;  // byte offset of the current raw stage
+    T* y = static_cast<T*>(a.y) + (row0 + w * L + tok(0)) * a.channels + g * per + cg0 + cl(0);
+    const int tiles = (a.seqlen + K * L - 1) / (K * L);
+    for (int tile = 0; tile < tiles; ++tile) {
+        const int tw = (tile * K + w) * L;
+        const bool past_end = tw + L > a.seqlen;
         // ---- this slice's (delta, delta u), B and C, in fp32 ----
         if (kCopy) copy_wait<1>();
         __syncwarp();
-        const char* raw = sm_raw + stage * Sh::RAW;
-        float skip[TPL], gate[TPL];
+        const char* raw = sm_raw + stage;
+        float skip[OWN], gate[OWN];
 #pragma unroll
-        for (int i = 0; i < TPL; ++i) {
-            float uf, d, zf;
+        for (int i = 0; i < OWN; i += VW) {
+            Pack<T, VW> ue, de, ze;
             if constexpr (kCopy) {
-                const T* e = reinterpret_cast<const T*>(raw) + (own + i) * CPW + ch;
-                uf = to_f32(e[0]), d = to_f32(e[kSlice * CPW]), zf = to_f32(e[2 * kSlice * CPW]);
+                const auto* e = reinterpret_cast<const Pack<T, VW>*>(raw + (tok(i) * CPW + cl(i)) * Sh::E);
+                ue = e[0], de = e[L * CPW / VW], ze = e[2 * L * CPW / VW];
             } else {
-                uf = to_f32(ru[i]), d = to_f32(rd[i]), zf = to_f32(rz[i]);
+#pragma unroll
+                for (int k = 0; k < VW; ++k) ue.v[k] = ru[i + k], de.v[k] = rd[i + k], ze.v[k] = rz[i + k];
             }
-            d += bias;
-            if (a.softplus) d = softplus(d);
-            if (tw + own + i >= a.seqlen) d = 0.f;  // past the end: a = 1 and no input
-            skip[i] = D * uf;
-            gate[i] = a.z ? silu_for<T>(zf) : 1.f;
-            const float du = d * uf;
-            *reinterpret_cast<float4*>(sm_pair + ch * PROW + 4 * (own + i)) = make_float4(d, d, du, du);
+            Pack<float, 2 * VW> pair;
+#pragma unroll
+            for (int k = 0; k < VW; ++k) {
+                const float uf = to_f32(ue.v[k]);
+                float d = to_f32(de.v[k]) + bias[i + k];
+                if (a.softplus) d = softplus(d);
+                if (past_end && tw + tok(i) >= a.seqlen) d = 0.f;  // a = 1 and no input
+                skip[i + k] = D[i + k] * uf;
+                gate[i + k] = a.z ? silu_for<T>(to_f32(ze.v[k])) : 1.f;
+                pair.v[2 * k] = d;
+                pair.v[2 * k + 1] = d * uf;
+            }
+            *reinterpret_cast<Pack<float, 2 * VW>*>(sm_pair + (tok(i) * CPW + cl(i)) * 2) = pair;
         }
         if constexpr (kCopy) {
 #pragma unroll
             for (int i = 0; i < Sh::BR; ++i) {
                 const int v = lane + 32 * i;
-                const Pack<T, Sh::BV> e = *reinterpret_cast<const Pack<T, Sh::BV>*>(raw + 3 * kSlice * Sh::ROW + v * 16);
+                if (Sh::BN % 32 == 0 || v < Sh::BN) {
+                    const Pack<T, Sh::BV> e =
+                        *reinterpret_cast<const Pack<T, Sh::BV>*>(raw + 3 * L * Sh::ROW + v * 16);
 #pragma unroll
-                for (int k = 0; k < Sh::BV; k += 4)
-                    *reinterpret_cast<float4*>(sm_bc + v * Sh::BV + k) = make_float4(
-                        to_f32(e.v[k]), to_f32(e.v[k + 1]), to_f32(e.v[k + 2]), to_f32(e.v[k + 3]));
+                    for (int k = 0; k < Sh::BV; k += 4)
+                        *reinterpret_cast<float4*>(sm_bc + v * Sh::BV + k) = make_float4(
+                            to_f32(e.v[k]), to_f32(e.v[k + 1]), to_f32(e.v[k + 2]), to_f32(e.v[k + 3]));
+                }
             }
+            fetch(tw + 2 * K * L, stage == 0 ? 2 * Sh::RAW : stage - Sh::RAW);
+            stage = stage == (kStages - 1) * Sh::RAW ? 0 : stage + Sh::RAW;
         } else {
             for (int i = lane; i < Sh::BC; i += 32) {
-                const int tok = i / (2 * NP), r = i % (2 * NP), n = r % NP, t = tw + tok;
+                const int r = i % (2 * NP), n = r % NP, t = tw + i / (2 * NP);
                 float v = 0.f;
                 if (n < N && t < a.seqlen) v = to_f32(r < NP ? B[t * a.bs_t + n] : C[t * a.cs_t + n]);
                 sm_bc[i] = v;
             }
+            fetch(tw + K * L, 0);
         }
-        if (kCopy) {
-            fetch(tw + 2 * K * kSlice, stage == 0 ? 2 : stage - 1);
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-        } else {
-            fetch(tw + K * kSlice, 0);
-        }
-        // sequences that start in this slice: lane i < kSlice looks at token tw + i
+        // sequences that start in this slice: lane i < L looks at token tw + i
         unsigned starts = 0u;
         int id = 0, id_before = -1;
         if (kSeq) {
-            const int t = min(tw + lane % kSlice, a.seqlen - 1);
+            const int t = min(tw + lane % L, a.seqlen - 1);
             id = seq_at(a.seq_idx, row0, t, a.nseq);
             if (t > 0) id_before = seq_at(a.seq_idx, row0, t - 1, a.nseq);
-            starts = __ballot_sync(0xffffffffu, lane < kSlice && tw + lane < a.seqlen && (t == 0 || id != id_before));
+            starts = __ballot_sync(0xffffffffu, lane < L && tw + lane < a.seqlen && (t == 0 || id != id_before));
         }
         __syncwarp();
-        // ---- the slice from zero: local state l, decay p, C l, and C p (kept) ----
-        float2 l[S2], p[S2], cp[kSlice][S2], acc[kSlice];
+        // ---- a and v of the slice ----
+        float2 av[L][CH][S2], hv[L][CH][S2];
 #pragma unroll
-        for (int j = 0; j < S2; ++j) l[j] = both(0.f), p[j] = both(1.f);
-#pragma unroll
-        for (int t = 0; t < kSlice; ++t) {
-            const float4 dd = *reinterpret_cast<const float4*>(sm_pair + ch * PROW + 4 * t);
-            const float4* Bt = reinterpret_cast<const float4*>(sm_bc + t * 2 * NP + ns * S);
-            const float4* Ct = reinterpret_cast<const float4*>(sm_bc + t * 2 * NP + NP + ns * S);
-            if (kSeq && (starts >> t & 1u)) {
-                init_state(l, __shfl_sync(0xffffffffu, id, t));
-#pragma unroll
-                for (int j = 0; j < S2; ++j) p[j] = both(0.f);
-            }
-            acc[t] = both(0.f);
+        for (int t = 0; t < L; ++t) {
+            const Pack<float, 2 * CH> d = *reinterpret_cast<const Pack<float, 2 * CH>*>(
+                sm_pair + (t * CPW + col * CH) * 2);  // delta, delta u of each channel
+            const Pack<float, S> Bt = *reinterpret_cast<const Pack<float, S>*>(sm_bc + t * 2 * NP + ns * S);
 #pragma unroll
             for (int j = 0; j < S2; ++j) {
-                const float2 x = __fmul2_rn(lo2(dd), A2[j]);
-                const float2 av = make_float2(exp2_fast(x.x), exp2_fast(x.y));
-                const float2 Bj = j % 2 ? hi2(Bt[j / 2]) : lo2(Bt[j / 2]), Cj = j % 2 ? hi2(Ct[j / 2]) : lo2(Ct[j / 2]);
-                l[j] = __ffma2_rn(av, l[j], __fmul2_rn(hi2(dd), Bj));
-                p[j] = __fmul2_rn(p[j], av);
-                acc[t] = __ffma2_rn(Cj, l[j], acc[t]);
-                cp[t][j] = __fmul2_rn(Cj, p[j]);
-            }
-        }
-        // ---- chain the slices: the state before this one, and before the next tile ----
-        float4* ep = sm_ep + (buf * K * 2) * S4 * 32 + lane;
 #pragma unroll
-        for (int j = 0; j < S4; ++j) {
-            ep[((w * 2 + 0) * S4 + j) * 32] = make_float4(l[2 * j].x, l[2 * j].y, l[2 * j + 1].x, l[2 * j + 1].y);
-            ep[((w * 2 + 1) * S4 + j) * 32] = make_float4(p[2 * j].x, p[2 * j].y, p[2 * j + 1].x, p[2 * j + 1].y);
-        }
-        __syncthreads();
-        float2 h[S2];
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            if (k == w) {
-#pragma unroll
-                for (int j = 0; j < S2; ++j) h[j] = h0[j];
-            }
-#pragma unroll
-            for (int j = 0; j < S4; ++j) {
-                const float4 e = ep[((k * 2 + 0) * S4 + j) * 32], q = ep[((k * 2 + 1) * S4 + j) * 32];
-                h0[2 * j] = __ffma2_rn(lo2(q), h0[2 * j], lo2(e));
-                h0[2 * j + 1] = __ffma2_rn(hi2(q), h0[2 * j + 1], hi2(e));
-            }
-        }
-        // ---- the read-out of the state before the slice ----
-        float out[kSlice];
-#pragma unroll
-        for (int t = 0; t < kSlice; ++t) {
-#pragma unroll
-            for (int j = 0; j < S2; ++j) acc[t] = __ffma2_rn(cp[t][j], h[j], acc[t]);
-            out[t] = acc[t].x + acc[t].y;
-        }
-        // ---- final states: of sequences that end inside the slice, and of the row's last ----
-        if (a.final_states) {
-            const bool last = tw < a.seqlen && tw + kSlice >= a.seqlen;
-            if (last) {
-#pragma unroll
-                for (int j = 0; j < S2; ++j) l[j] = __ffma2_rn(p[j], h[j], l[j]);
-                const int s = kSeq ? __shfl_sync(0xffffffffu, id, a.seqlen - 1 - tw) : 0;
-                write_state(l, s);
-                keep(s + 1, a.nseq);
-            }
-            if (kSeq && starts) {  // rare: walk the slice again from its true state
-                for (int t = 0; t < kSlice; ++t) {
-                    if (starts >> t & 1u) {
-                        const int s = __shfl_sync(0xffffffffu, id, t), before = __shfl_sync(0xffffffffu, id_before, t);
-                        if (before >= 0) write_state(h, before);
-                        keep(before + 1, s);
-                        init_state(h, s);
-                    }
-                    const float4 dd = *reinterpret_cast<const float4*>(sm_pair + ch * PROW + 4 * t);
-#pragma unroll
-                    for (int j = 0; j < S2; ++j) {
-                        const float2 Bj = *reinterpret_cast<const float2*>(sm_bc + t * 2 * NP + ns * S + 2 * j);
-                        const float2 x = __fmul2_rn(lo2(dd), A2[j]);
-                        h[j] = __ffma2_rn(make_float2(exp2_fast(x.x), exp2_fast(x.y)), h[j], __fmul2_rn(hi2(dd), Bj));
-                    }
+                for (int m = 0; m < CH; ++m) {
+                    av[t][m][j] = make_float2(exp2_fast(d.v[2 * m] * A2[m][j].x), exp2_fast(d.v[2 * m] * A2[m][j].y));
+                    hv[t][m][j] = make_float2(d.v[2 * m + 1] * Bt.v[2 * j], d.v[2 * m + 1] * Bt.v[2 * j + 1]);
                 }
             }
         }
-        // ---- sum over the channel's lanes; each ends with the tokens it owns ----
+        // ---- the recurrence: the state from the slice before, through this one, to the next ----
+        State h;
+        if (w == 0 && tile == 0) {
+            if (kSeq) {
 #pragma unroll
-        for (int m = LN / 2, n = kSlice; m >= 1; m /= 2) {
-            if (n > 1) {  // keep the half of the tokens that the lane's side owns
+                for (int m = 0; m < CH; ++m)
+#pragma unroll
+                    for (int j = 0; j < S2; ++j) h[m][j] = make_float2(0.f, 0.f);
+            } else {
+                init_state(h, 0);
+            }
+        } else {
+            asm volatile("barrier.sync %0, 64;" ::"r"(w) : "memory");  // with the arrival of warp w - 1
+#pragma unroll
+            for (int i = 0; i < CH * S / 4; ++i) {
+                const float4 q = sm_state[i * 32];
+                h[4 * i / S][4 * i % S / 2] = make_float2(q.x, q.y);
+                h[4 * i / S][4 * i % S / 2 + 1] = make_float2(q.z, q.w);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < L; ++t) {
+            if (kSeq && (starts >> t & 1u)) {
+                const int s = __shfl_sync(0xffffffffu, id, t), before = __shfl_sync(0xffffffffu, id_before, t);
+                if (a.final_states) {
+                    if (before >= 0) write_state(h, before);
+                    keep(before + 1, s);
+                }
+                init_state(h, s);
+            }
+#pragma unroll
+            for (int m = 0; m < CH; ++m)
+#pragma unroll
+                for (int j = 0; j < S2; ++j) h[m][j] = hv[t][m][j] = __ffma2_rn(av[t][m][j], h[m][j], hv[t][m][j]);
+        }
+        if (w < K - 1 || tile < tiles - 1) {
+            const int next = w == K - 1 ? 0 : w + 1;
+#pragma unroll
+            for (int i = 0; i < CH * S / 4; ++i) {
+                const float2 lo = h[4 * i / S][4 * i % S / 2], hi = h[4 * i / S][4 * i % S / 2 + 1];
+                sm_next[i * 32] = make_float4(lo.x, lo.y, hi.x, hi.y);
+            }
+            asm volatile("barrier.arrive %0, 64;" ::"r"(next) : "memory");
+        }
+        if (a.final_states && tw < a.seqlen && tw + L >= a.seqlen) {  // this slice has the row's last token
+            const int s = kSeq ? __shfl_sync(0xffffffffu, id, a.seqlen - 1 - tw) : 0;
+            write_state(h, s);
+            keep(s + 1, a.nseq);
+        }
+        // ---- read-out, summed over a column's lanes; each ends with the sums it owns ----
+        float out[Sh::OUTS];
+#pragma unroll
+        for (int t = 0; t < L; ++t) {
+            const Pack<float, S> Ct = *reinterpret_cast<const Pack<float, S>*>(sm_bc + t * 2 * NP + NP + ns * S);
+            float2 acc[CH];
+#pragma unroll
+            for (int j = 0; j < S2; ++j) {
+                const float2 Cj = make_float2(Ct.v[2 * j], Ct.v[2 * j + 1]);
+#pragma unroll
+                for (int m = 0; m < CH; ++m)
+                    acc[m] = j == 0 ? __fmul2_rn(Cj, hv[t][m][j]) : __ffma2_rn(Cj, hv[t][m][j], acc[m]);
+            }
+#pragma unroll
+            for (int m = 0; m < CH; ++m) out[t * CH + m] = acc[m].x + acc[m].y;
+        }
+#pragma unroll
+        for (int k = Sh::LN / 2, n = Sh::OUTS; k >= 1; k /= 2) {
+            if (n > 1) {  // keep the half of the sums that the lane's side owns
                 n /= 2;
-                const bool up = ns & m;
+                const bool up = ns & k;
 #pragma unroll
                 for (int i = 0; i < n; ++i) {
                     const float give = up ? out[i] : out[i + n], stay = up ? out[i + n] : out[i];
-                    out[i] = stay + __shfl_xor_sync(0xffffffffu, give, m * CPW);
+                    out[i] = stay + __shfl_xor_sync(0xffffffffu, give, k * COLS);
                 }
             } else {
-                out[0] += __shfl_xor_sync(0xffffffffu, out[0], m * CPW);
+                out[0] += __shfl_xor_sync(0xffffffffu, out[0], k * COLS);
             }
         }
-        if (owner) {
 #pragma unroll
-            for (int i = 0; i < TPL; ++i) {
-                const int t = tw + own + i;
-                if (t < a.seqlen) y[(int64_t)t * a.channels] = from_f32<T>((out[i] + skip[i]) * gate[i]);
+        for (int i = 0; i < OWN; i += VW) {
+            T* yi = y + (int64_t)(tok(i) - tok(0)) * a.channels + (cl(i) - cl(0));
+            Pack<T, VW> v;
+#pragma unroll
+            for (int k = 0; k < VW; ++k) v.v[k] = from_f32<T>((out[i + k] + skip[i + k]) * gate[i + k]);
+            if (past_end && tw + tok(i) >= a.seqlen) continue;
+            if (kCopy) {  // rows of whole 16-byte parts: a pair of channels is inside or outside as one
+                if (mine[i]) *reinterpret_cast<Pack<T, VW>*>(yi) = v;
+            } else {
+#pragma unroll
+                for (int k = 0; k < VW; ++k)
+                    if (mine[i + k]) yi[k] = v.v[k];
             }
         }
+        y += (int64_t)(K * L) * a.channels;
     }
 }
 
@@ -447,57 +488,59 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Sele
     static_cast<T*>(a.y)[(int64_t)b * a.channels + c] = from_f32<T>(y);
 }
 
-template <typename T, int S, int LN, int K, bool kSeq, bool kCopy>
+template <typename T, typename Sh, int kMinCtas, bool kSeq, bool kCopy>
 cudaError_t start_scan(const SelectiveArgs& a, cudaStream_t st) {
-    using Sh = ScanShape<T, S, LN, K>;
     constexpr int smem = Sh::smem(kCopy);
     static_assert(smem <= 227 * 1024, "fits one SM");
     const int per = a.channels / a.ngroups, units = (per + Sh::CPW - 1) / Sh::CPW;
     const unsigned grid = (unsigned)((int64_t)a.batch * a.ngroups * units);
-    const auto kernel = selective_scan_kernel<T, S, LN, K, kSeq, kCopy>;
+    const auto kernel = selective_scan_kernel<T, Sh, kMinCtas, kSeq, kCopy>;
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<grid, 32 * K, smem, st>>>(a, units);
+    kernel<<<grid, 32 * Sh::K, smem, st>>>(a, units);
     return cudaGetLastError();
 }
 
-template <typename T, int S, int LN, int K>
+template <typename T, typename Sh, int kMinCtas>
 cudaError_t run_scan(const SelectiveArgs& a, cudaStream_t st) {
-    using Sh = ScanShape<T, S, LN, K>;
     if constexpr (Sh::kCanCopy) {
         VectorRule tok(sizeof(T)), bc(sizeof(T));
         tok.address(a.u).address(a.dt).elements(a.us_b).elements(a.us_t).elements(a.ds_b).elements(a.ds_t);
         if (a.z) tok.address(a.z).elements(a.zs_b).elements(a.zs_t);
-        tok.elements(a.channels / a.ngroups);
+        tok.address(a.y).elements(a.channels / a.ngroups);
         bc.address(a.B).address(a.C).elements(a.bs_b).elements(a.bs_t).elements(a.cs_b).elements(a.cs_t);
         bc.elements(a.dstate);
         if (tok.multiple_of(Sh::TB) && bc.multiple_of(16))
-            return a.seq_idx ? start_scan<T, S, LN, K, true, true>(a, st) : start_scan<T, S, LN, K, false, true>(a, st);
+            return a.seq_idx ? start_scan<T, Sh, kMinCtas, true, true>(a, st)
+                             : start_scan<T, Sh, kMinCtas, false, true>(a, st);
     }
-    return a.seq_idx ? start_scan<T, S, LN, K, true, false>(a, st) : start_scan<T, S, LN, K, false, false>(a, st);
+    return a.seq_idx ? start_scan<T, Sh, kMinCtas, true, false>(a, st)
+                     : start_scan<T, Sh, kMinCtas, false, false>(a, st);
 }
 
-template <typename T, int S, int LN>
-cudaError_t scan_by_slices(const SelectiveArgs& a, cudaStream_t st) {
-    const int64_t units = (int64_t)a.batch * a.ngroups * ((a.channels / a.ngroups + 32 / LN - 1) / (32 / LN));
-    // 16 warps per CTA where the CTAs do not fill the GPU's SMs twice, else 4
-    if constexpr (S * LN <= 64) {
-        if (units < 2 * 148 && a.seqlen > 4 * kSlice) return run_scan<T, S, LN, 16>(a, st);
-    }
-    return run_scan<T, S, LN, 4>(a, st);
+constexpr int64_t kManyCtas = 2 * 148;  // CTAs of 4 warps that keep every SM busy
+
+template <typename T, int LN>
+cudaError_t scan_by_size(const SelectiveArgs& a, cudaStream_t st) {
+    const int64_t per = a.channels / a.ngroups, rows = (int64_t)a.batch * a.ngroups;
+    const int64_t units = rows * ((per * LN + 63) / 64);  // CTAs with two channels per lane
+    if (units >= kManyCtas) return run_scan<T, ScanShape<T, 2, 4, LN, 4, 4>, 4>(a, st);
+    if (units * 2 >= kManyCtas) return run_scan<T, ScanShape<T, 1, 4, LN, 8, 4>, 5>(a, st);
+    if constexpr (LN <= 16) return run_scan<T, ScanShape<T, 1, 4, LN, 8, 16>, 1>(a, st);
+    return run_scan<T, ScanShape<T, 1, 4, LN, 8, 8>, 1>(a, st);
 }
 
 template <typename T>
 cudaError_t scan_by_states(const SelectiveArgs& a, cudaStream_t st) {
-    if (a.dstate <= 8) return scan_by_slices<T, 4, 2>(a, st);
-    if (a.dstate <= 16) return scan_by_slices<T, 4, 4>(a, st);
-    if (a.dstate <= 32) return scan_by_slices<T, 4, 8>(a, st);
-    if (a.dstate <= 64) return scan_by_slices<T, 4, 16>(a, st);
-    if (a.dstate <= 128) return scan_by_slices<T, 4, 32>(a, st);
-    return scan_by_slices<T, 8, 32>(a, st);
+    if (a.dstate <= 8) return scan_by_size<T, 2>(a, st);
+    if (a.dstate <= 16) return scan_by_size<T, 4>(a, st);
+    if (a.dstate <= 32) return scan_by_size<T, 8>(a, st);
+    if (a.dstate <= 64) return scan_by_size<T, 16>(a, st);
+    if (a.dstate <= 128) return scan_by_size<T, 32>(a, st);
+    return run_scan<T, ScanShape<T, 1, 8, 32, 4, 4>, 2>(a, st);
 }
 
 }  // namespace
