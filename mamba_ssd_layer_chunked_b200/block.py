@@ -10,7 +10,6 @@ that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Sequence, Tuple, Union
 
@@ -21,35 +20,41 @@ from . import ssd as _ssd
 _DTYPES = {torch.float32: _ssd.SSD_DTYPE_F32, torch.bfloat16: _ssd.SSD_DTYPE_BF16}
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 _i64 = ctypes.c_int64
-_HERE = contextlib.nullcontext()
+_INVALID_SIZE = ctypes.c_size_t(-1).value
+_fn = None  # the loaded library
 
 
 class ConvProblem(ctypes.Structure):
-    """Mirror of ssd_conv_problem."""
+    """Mirror of ssd_conv_problem (its small arrays as one field per element)."""
 
     _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("width", _i64), ("nseq", _i64),
-                ("x_stride", _i64 * 2), ("split", _i64 * 3), ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
+                ("x_batch_stride", _i64), ("x_token_stride", _i64), ("split0", _i64), ("split1", _i64),
+                ("split2", _i64), ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
 
 
 class SelectiveProblem(ctypes.Structure):
     """Mirror of ssd_selective_problem."""
 
     _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("dstate", _i64), ("ngroups", _i64),
-                ("nseq", _i64), ("u_stride", _i64 * 2), ("dt_stride", _i64 * 2), ("z_stride", _i64 * 2),
-                ("B_stride", _i64 * 2), ("C_stride", _i64 * 2), ("dtype", ctypes.c_int),
-                ("dt_softplus", ctypes.c_int32)]
+                ("nseq", _i64), ("u_batch_stride", _i64), ("u_token_stride", _i64), ("dt_batch_stride", _i64),
+                ("dt_token_stride", _i64), ("z_batch_stride", _i64), ("z_token_stride", _i64),
+                ("B_batch_stride", _i64), ("B_token_stride", _i64), ("C_batch_stride", _i64),
+                ("C_token_stride", _i64), ("dtype", ctypes.c_int), ("dt_softplus", ctypes.c_int32)]
 
 
 class NormProblem(ctypes.Structure):
     """Mirror of ssd_norm_problem."""
 
-    _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("ngroups", _i64), ("x_stride", _i64 * 2),
-                ("z_stride", _i64 * 2), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("ngroups", _i64),
+                ("x_batch_stride", _i64), ("x_token_stride", _i64), ("z_batch_stride", _i64),
+                ("z_token_stride", _i64), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
                 ("eps", ctypes.c_float), ("alpha", ctypes.c_float), ("gate_first", ctypes.c_int32)]
 
 
 def declare(lib):
-    """Argument types of the C functions this module calls."""
+    """Take the loaded library, and declare the argument types of the C functions this module calls."""
+    global _fn
+    _fn = lib
     vp, P = ctypes.c_void_p, ctypes.POINTER
     for name, argtypes, restype in (
             ("ssd_causal_conv", [P(ConvProblem)] + [vp] * 10, ctypes.c_int),
@@ -85,29 +90,29 @@ def _need(t: Optional[torch.Tensor], name: str, shape, dtype, device, dense=True
     if dense:
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-    elif t.shape[-1] > 1 and t.stride(-1) != 1:
+    elif t.stride(-1) != 1 and shape[-1] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     return t.data_ptr()
 
 
-def _lead(x: torch.Tensor, name: str):
-    """The device of the call's first tensor, which must be a CUDA tensor."""
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(x: torch.Tensor, stream) -> bool:
+    """Whether a call on x has to change the current device or stream first."""
+    return stream is not None or not x.is_cuda or x.get_device() != _current_device()
+
+
+def _run_on(x: torch.Tensor, stream):
+    """A context in which x's device is current, and `stream` where it is given."""
     if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return x.device
-
-
-def _run_on(device: torch.device, stream):
-    """A context in which `device` is current, and `stream` where it is given."""
-    if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        return torch.cuda.stream(stream)
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _raw_stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if stream is None:
+        return torch.cuda.device(x.device)
+    if stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    return torch.cuda.stream(stream)
 
 
 def _nseq(seq_idx, nseq) -> int:
@@ -116,6 +121,12 @@ def _nseq(seq_idx, nseq) -> int:
             raise ValueError("nseq is required with seq_idx (the number of sequences per row)")
         return 1
     return int(nseq)
+
+
+def _activation(name) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be 'silu' or None, not {name!r}")
+    return _ACTIVATIONS[name]
 
 
 def _split(channels: int, splits: Optional[Sequence[int]]):
@@ -129,16 +140,18 @@ def _split(channels: int, splits: Optional[Sequence[int]]):
 
 def _outputs(lead, split, x, out, as_tuple):
     """The outputs' tensors (allocated, or checked) and their three addresses."""
-    shapes = [torch.Size((*lead, n)) for n in split if n]
     if out is None:
-        outs = tuple(torch.empty(s, dtype=x.dtype, device=x.device) for s in shapes)
+        outs = [x.new_empty((*lead, n)) for n in split if n]
         ptrs = [o.data_ptr() for o in outs]
     else:
         outs = tuple(out) if as_tuple else (out,)
+        shapes = [(*lead, n) for n in split if n]
         if len(outs) != len(shapes):
             raise ValueError(f"out must hold {len(shapes)} tensors")
         ptrs = [_need(o, f"out[{i}]", s, x.dtype, x.device) for i, (o, s) in enumerate(zip(outs, shapes))]
-    return outs, ptrs + [None] * (3 - len(ptrs))
+    while len(ptrs) < 3:
+        ptrs.append(None)
+    return (tuple(outs) if as_tuple else outs[0]), ptrs
 
 
 Outputs = Union[torch.Tensor, Tuple[torch.Tensor, ...]]
@@ -163,33 +176,27 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     unless return_final_states."""
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("shapes: x [b,T,C], weight [C,W]")
-    device, dtype = _lead(x, "x"), _dtype(x, "x")
+    if _elsewhere(x, stream):
+        with _run_on(x, stream):
+            return causal_conv(x, weight, bias, init_states, seq_idx, nseq, activation, splits, return_final_states,
+                               out, final_out)
+    device, dtype = x.device, x.dtype
     b, T, C = x.shape
     W, nseq = weight.shape[1], _nseq(seq_idx, nseq)
-    if C > 1 and x.stride(2) != 1:
-        raise ValueError("the last dimension of x must be contiguous")
-    split = _split(C, splits)
-    windows = torch.Size((b, nseq, W - 1, C))
-    ptrs = (x.data_ptr(), _need(weight, "weight", (C, W), torch.float32, device),
-            _need(bias, "bias", (C,), torch.float32, device),
-            _need(init_states, "init_states", windows, x.dtype, device),
+    split, windows = _split(C, splits), (b, nseq, W - 1, C)
+    xp = _need(x, "x", x.shape, dtype, device, False)
+    p = ConvProblem(b, T, C, W, nseq, x.stride(0), x.stride(1), *split, _dtype(x, "x"), _activation(activation))
+    ptrs = (_need(weight, "weight", (C, W), torch.float32, device), _need(bias, "bias", (C,), torch.float32, device),
+            _need(init_states, "init_states", windows, dtype, device),
             _need(seq_idx, "seq_idx", (b, T), torch.int32, device))
-    p = ConvProblem(b, T, C, W, nseq, (x.stride(0), x.stride(1)), split, dtype, _activation(activation))
-    with _run_on(device, stream):
-        outs, outp = _outputs((b, T), split, x, out, splits is not None)
-        final, finp = None, None
-        if return_final_states:
-            final = torch.empty(windows, dtype=x.dtype, device=device) if final_out is None else final_out
-            finp = _need(final, "final_out", windows, x.dtype, device)
-        st = _ssd.lib().ssd_causal_conv(ctypes.byref(p), *ptrs, *outp, finp, _raw_stream(device))
-    _ssd._check(st, "ssd_causal_conv")
-    return (outs if splits is not None else outs[0]), final
-
-
-def _activation(name) -> int:
-    if name not in _ACTIVATIONS:
-        raise ValueError(f"activation must be 'silu' or None, not {name!r}")
-    return _ACTIVATIONS[name]
+    outs, outp = _outputs((b, T), split, x, out, splits is not None)
+    final, finp = None, None
+    if return_final_states:
+        final = x.new_empty(windows) if final_out is None else final_out
+        finp = _need(final, "final_out", windows, dtype, device)
+    _ssd._check(_fn.ssd_causal_conv(ctypes.byref(p), xp, *ptrs, *outp, finp, _raw_stream(device.index)),
+                "ssd_causal_conv")
+    return outs, final
 
 
 def conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -200,44 +207,45 @@ def conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: 
     of [b, splits[i]] with splits."""
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("shapes: x [b,C], weight [C,W]")
-    device, dtype = _lead(x, "x"), _dtype(x, "x")
+    if _elsewhere(x, stream):
+        with _run_on(x, stream):
+            return conv_step(x, state, weight, bias, activation, splits, out)
+    device, dtype = x.device, x.dtype
     b, C = x.shape
     W = weight.shape[1]
-    if C > 1 and x.stride(1) != 1:
-        raise ValueError("the last dimension of x must be contiguous")
     split = _split(C, splits)
-    ptrs = (x.data_ptr(), _need(weight, "weight", (C, W), torch.float32, device),
-            _need(bias, "bias", (C,), torch.float32, device), _need(state, "state", (b, W - 1, C), x.dtype, device))
-    p = ConvProblem(b, 1, C, W, 1, (x.stride(0), 0), split, dtype, _activation(activation))
-    with _run_on(device, stream):
-        outs, outp = _outputs((b,), split, x, out, splits is not None)
-        st = _ssd.lib().ssd_conv_step(ctypes.byref(p), *ptrs, *outp, _raw_stream(device))
-    _ssd._check(st, "ssd_conv_step")
-    return outs if splits is not None else outs[0]
+    xp = _need(x, "x", x.shape, dtype, device, False)
+    p = ConvProblem(b, 1, C, W, 1, x.stride(0), 0, *split, _dtype(x, "x"), _activation(activation))
+    ptrs = (_need(weight, "weight", (C, W), torch.float32, device), _need(bias, "bias", (C,), torch.float32, device),
+            _need(state, "state", (b, W - 1, C), dtype, device))
+    outs, outp = _outputs((b,), split, x, out, splits is not None)
+    _ssd._check(_fn.ssd_conv_step(ctypes.byref(p), xp, *ptrs, *outp, _raw_stream(device.index)), "ssd_conv_step")
+    return outs
 
 
 # ---- the selective scan ----------------------------------------------------------
 
-def _selective(u, dt, A, B, C, D, z, dt_bias, lead):
+def _selective(u, dt, A, B, C, D, z, dt_bias):
     """Checked addresses (u, dt, A, B, C, D, z, dt_bias), sizes and strides of a selective call."""
-    k = len(lead)
-    device = _lead(u, "u")
-    _dtype(u, "u")
-    ch = u.shape[-1]
+    dtype, device, acts = u.dtype, u.device, u.shape
+    k, ch = len(acts) - 1, acts[-1]
     if A.dim() != 2 or B.dim() != k + 2:
         raise ValueError("shapes: A [channels,N], B and C [b,T,G,N] ([b,G,N] for a step)")
     N, G = A.shape[1], B.shape[-2]
-    acts, bc = torch.Size((*lead, ch)), torch.Size((*lead, G, N))
-    for t, name in ((B, "B"), (C, "C")):
-        if t.dim() == k + 2 and G > 1 and t.stride(-2) != N:
-            raise ValueError(f"the groups of {name} must be contiguous (stride N)")
-    f32 = torch.float32
-    ptrs = (_need(u, "u", acts, u.dtype, device, False), _need(dt, "dt", acts, u.dtype, device, False),
-            _need(A, "A", (ch, N), f32, device), _need(B, "B", bc, u.dtype, device, False),
-            _need(C, "C", bc, u.dtype, device, False), _need(D, "D", (ch,), f32, device),
-            _need(z, "z", acts, u.dtype, device, False), _need(dt_bias, "dt_bias", (ch,), f32, device))
-    strides = [(t.stride(0), t.stride(1) if k == 2 else 0) if t is not None else (0, 0) for t in (u, dt, z, B, C)]
-    return ptrs, (ch, N, G), strides
+    bc, f32 = (*acts[:-1], G, N), torch.float32
+    ptrs = (_need(u, "u", acts, dtype, device, False), _need(dt, "dt", acts, dtype, device, False),
+            _need(A, "A", (ch, N), f32, device), _need(B, "B", bc, dtype, device, False),
+            _need(C, "C", bc, dtype, device, False), _need(D, "D", (ch,), f32, device),
+            _need(z, "z", acts, dtype, device, False), _need(dt_bias, "dt_bias", (ch,), f32, device))
+    if G > 1 and (B.stride(-2) != N or C.stride(-2) != N):
+        raise ValueError("the groups of B and of C must be contiguous (stride N)")
+    strides = []
+    for t in (u, dt, z, B, C):
+        if t is None:
+            strides += (0, 0)
+        else:
+            strides += (t.stride(0), t.stride(1) if k == 2 else 0)
+    return ptrs, ch, N, G, strides
 
 
 def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
@@ -259,28 +267,32 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     takes dt + dt_bias as delta."""
     if u.dim() != 3:
         raise ValueError("u must be [b, T, channels]")
-    b, T = u.shape[:2]
-    ptrs, (ch, N, G), strides = _selective(u, dt, A, B, C, D, z, dt_bias, (b, T))
-    nseq, device = _nseq(seq_idx, nseq), u.device
-    states = torch.Size((b, nseq, N, ch))
+    if _elsewhere(u, stream):
+        with _run_on(u, stream):
+            return selective_scan(u, dt, A, B, C, D, z, dt_bias, dt_softplus, init_states, seq_idx, nseq,
+                                  return_final_states, out, final_out, workspace)
+    dtype = _dtype(u, "u")
+    ptrs, ch, N, G, strides = _selective(u, dt, A, B, C, D, z, dt_bias)
+    (b, T, _), device, nseq = u.shape, u.device, _nseq(seq_idx, nseq)
+    states = (b, nseq, N, ch)
     initp = _need(init_states, "init_states", states, torch.float32, device)
     idsp = _need(seq_idx, "seq_idx", (b, T), torch.int32, device)
-    p = SelectiveProblem(b, T, ch, N, G, nseq, *strides, _DTYPES[u.dtype], int(bool(dt_softplus)))
-    lib = _ssd.lib()
-    with _run_on(device, stream):
-        y = torch.empty((b, T, ch), dtype=u.dtype, device=device) if out is None else out
-        yp = _need(y, "out", (b, T, ch), u.dtype, device)
-        final, finp = None, None
-        if return_final_states:
-            final = torch.empty(states, dtype=torch.float32, device=device) if final_out is None else final_out
-            finp = _need(final, "final_out", states, torch.float32, device)
-        need = lib.ssd_selective_scan_workspace_bytes(ctypes.byref(p))
-        if workspace is None and 0 < need < ctypes.c_size_t(-1).value:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        wsp = None if workspace is None else _need(workspace, "workspace", workspace.shape, workspace.dtype, device)
-        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.ssd_selective_scan(ctypes.byref(p), *ptrs, initp, idsp, yp, finp, wsp, size, _raw_stream(device))
-    _ssd._check(st, "ssd_selective_scan")
+    p = ctypes.byref(SelectiveProblem(b, T, ch, N, G, nseq, *strides, dtype, 1 if dt_softplus else 0))
+    y = u.new_empty(u.shape) if out is None else out
+    yp = _need(y, "out", u.shape, u.dtype, device)
+    final, finp = None, None
+    if return_final_states:
+        final = u.new_empty(states, dtype=torch.float32) if final_out is None else final_out
+        finp = _need(final, "final_out", states, torch.float32, device)
+    need = _fn.ssd_selective_scan_workspace_bytes(p)
+    if workspace is None and 0 < need < _INVALID_SIZE:
+        workspace = u.new_empty(need, dtype=torch.uint8)
+    wsp, size = None, 0
+    if workspace is not None:
+        wsp = _need(workspace, "workspace", workspace.shape, workspace.dtype, device)
+        size = workspace.numel() * workspace.element_size()
+    _ssd._check(_fn.ssd_selective_scan(p, *ptrs, initp, idsp, yp, finp, wsp, size, _raw_stream(device.index)),
+                "ssd_selective_scan")
     return y, final
 
 
@@ -293,32 +305,32 @@ def selective_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     Returns y [b, channels]."""
     if u.dim() != 2:
         raise ValueError("u must be [b, channels]")
-    b = u.shape[0]
-    ptrs, (ch, N, G), strides = _selective(u, dt, A, B, C, D, z, dt_bias, (b,))
-    device = u.device
+    if _elsewhere(u, stream):
+        with _run_on(u, stream):
+            return selective_step(u, dt, A, B, C, state, D, z, dt_bias, dt_softplus, out)
+    dtype = _dtype(u, "u")
+    ptrs, ch, N, G, strides = _selective(u, dt, A, B, C, D, z, dt_bias)
+    b, device = u.shape[0], u.device
     sp = _need(state, "state", (b, N, ch), torch.float32, device)
-    p = SelectiveProblem(b, 1, ch, N, G, 1, *strides, _DTYPES[u.dtype], int(bool(dt_softplus)))
-    with _run_on(device, stream):
-        y = torch.empty((b, ch), dtype=u.dtype, device=device) if out is None else out
-        yp = _need(y, "out", (b, ch), u.dtype, device)
-        st = _ssd.lib().ssd_selective_step(ctypes.byref(p), *ptrs, sp, yp, _raw_stream(device))
-    _ssd._check(st, "ssd_selective_step")
+    p = SelectiveProblem(b, 1, ch, N, G, 1, *strides, dtype, 1 if dt_softplus else 0)
+    y = u.new_empty(u.shape) if out is None else out
+    yp = _need(y, "out", u.shape, u.dtype, device)
+    _ssd._check(_fn.ssd_selective_step(ctypes.byref(p), *ptrs, sp, yp, _raw_stream(device.index)),
+                "ssd_selective_step")
     return y
 
 
 # ---- norms -------------------------------------------------------------------------
 
-def _rows(x: torch.Tensor, name: str):
-    """(batch, tokens) of a tensor [rows, channels] or [b, T, channels]."""
-    if x.dim() not in (2, 3):
-        raise ValueError(f"{name} must be [rows, channels] or [b, T, channels]")
-    return (1, x.shape[0]) if x.dim() == 2 else (x.shape[0], x.shape[1])
-
-
-def _row_strides(t: Optional[torch.Tensor]):
-    if t is None:
-        return (0, 0)
-    return (0, t.stride(0)) if t.dim() == 2 else (t.stride(0), t.stride(1))
+def _rows(x: torch.Tensor, z: Optional[torch.Tensor]):
+    """batch, tokens, channels, and the two strides of x and of z (of x's shape, or None)."""
+    if x.dim() == 3:
+        zs = (z.stride(0), z.stride(1)) if z is not None else (0, 0)
+        return (*x.shape, x.stride(0), x.stride(1)), zs
+    if x.dim() == 2:
+        zs = (0, z.stride(0)) if z is not None else (0, 0)
+        return (1, *x.shape, 0, x.stride(0)), zs
+    raise ValueError("x must be [rows, channels] or [b, T, channels]")
 
 
 def gated_norm(x: torch.Tensor, weight: torch.Tensor, z: Optional[torch.Tensor] = None, ngroups: int = 1,
@@ -328,18 +340,18 @@ def gated_norm(x: torch.Tensor, weight: torch.Tensor, z: Optional[torch.Tensor] 
     weight [channels] fp32, of x * silu(z) (gate_first), or of x and times silu(z)
     afterwards; without z the plain norm. x and z [rows, channels] or
     [b, T, channels] in one dtype (float32 or bfloat16), which the result has too."""
-    device, dtype = _lead(x, "x"), _dtype(x, "x")
-    b, T = _rows(x, "x")
-    ch = x.shape[-1]
-    ptrs = (_need(x, "x", x.shape, x.dtype, device, False), _need(z, "z", x.shape, x.dtype, device, False),
-            _need(weight, "weight", (ch,), torch.float32, device))
-    p = NormProblem(b, T, ch, int(ngroups), _row_strides(x), _row_strides(z), dtype, dtype, eps, 1.0,
-                    int(bool(gate_first)))
-    with _run_on(device, stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
-        yp = _need(y, "out", x.shape, x.dtype, device)
-        st = _ssd.lib().ssd_gated_norm(ctypes.byref(p), *ptrs, yp, _raw_stream(device))
-    _ssd._check(st, "ssd_gated_norm")
+    if _elsewhere(x, stream):
+        with _run_on(x, stream):
+            return gated_norm(x, weight, z, ngroups, eps, gate_first, out)
+    dtype, device, shape = x.dtype, x.device, x.shape
+    xp, zp = _need(x, "x", shape, dtype, device, False), _need(z, "z", shape, dtype, device, False)
+    (b, T, ch, xs0, xs1), zs = _rows(x, z)
+    wp = _need(weight, "weight", (ch,), torch.float32, device)
+    code = _dtype(x, "x")
+    p = NormProblem(b, T, ch, int(ngroups), xs0, xs1, *zs, code, code, eps, 1.0, 1 if gate_first else 0)
+    y = x.new_empty(shape) if out is None else out
+    yp = _need(y, "out", shape, dtype, device)
+    _ssd._check(_fn.ssd_gated_norm(ctypes.byref(p), xp, zp, wp, yp, _raw_stream(device.index)), "ssd_gated_norm")
     return y
 
 
@@ -355,25 +367,24 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     scale a number or an fp32 tensor [channels]; the residual is fp32 or of x's
     dtype (without one, r has residual_dtype, fp32 by default). The norm is taken of
     the unrounded sum. residual_out=residual updates a dense residual in place."""
-    device, dtype = _lead(x, "x"), _dtype(x, "x")
-    b, T = _rows(x, "x")
-    ch = x.shape[-1]
+    if _elsewhere(x, stream):
+        with _run_on(x, stream):
+            return add_norm(x, weight, residual, scale, eps, residual_dtype, out, residual_out)
+    dtype, device, shape, code = x.dtype, x.device, x.shape, _dtype(x, "x")
     rdt = residual.dtype if residual is not None else (residual_dtype or torch.float32)
     if residual_dtype is not None and residual_dtype != rdt:
         raise TypeError(f"residual_dtype is {residual_dtype}, the residual {rdt}")
-    if rdt not in (torch.float32, x.dtype):
-        raise TypeError(f"the residual must be float32 or {x.dtype}, not {rdt}")
-    per_channel = isinstance(scale, torch.Tensor)
-    ptrs = (_need(x, "x", x.shape, x.dtype, device, False),
-            _need(residual, "residual", x.shape, rdt, device, False),
-            _need(weight, "weight", (ch,), torch.float32, device),
-            _need(scale, "scale", (ch,), torch.float32, device) if per_channel else None)
-    p = NormProblem(b, T, ch, 1, _row_strides(x), _row_strides(residual), dtype, _DTYPES[rdt], eps,
-                    1.0 if per_channel else scale, 0)
-    with _run_on(device, stream):
-        y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
-        r = torch.empty(x.shape, dtype=rdt, device=device) if residual_out is None else residual_out
-        yp, rp = _need(y, "out", x.shape, x.dtype, device), _need(r, "residual_out", x.shape, rdt, device)
-        st = _ssd.lib().ssd_add_norm(ctypes.byref(p), *ptrs, yp, rp, _raw_stream(device))
-    _ssd._check(st, "ssd_add_norm")
+    if rdt is not torch.float32 and rdt is not dtype:
+        raise TypeError(f"the residual must be float32 or {dtype}, not {rdt}")
+    xp, rp = _need(x, "x", shape, dtype, device, False), _need(residual, "residual", shape, rdt, device, False)
+    (b, T, ch, xs0, xs1), rs = _rows(x, residual)
+    wp, sp = _need(weight, "weight", (ch,), torch.float32, device), None
+    per_channel = isinstance(scale, torch.Tensor)  # not rebound: the tensor lives until the launch
+    if per_channel:
+        sp = _need(scale, "scale", (ch,), torch.float32, device)
+    p = NormProblem(b, T, ch, 1, xs0, xs1, *rs, code, _DTYPES[rdt], eps, 1.0 if per_channel else scale, 0)
+    y = x.new_empty(shape) if out is None else out
+    r = x.new_empty(shape, dtype=rdt) if residual_out is None else residual_out
+    yp, rop = _need(y, "out", shape, dtype, device), _need(r, "residual_out", shape, rdt, device)
+    _ssd._check(_fn.ssd_add_norm(ctypes.byref(p), xp, rp, wp, sp, yp, rop, _raw_stream(device.index)), "ssd_add_norm")
     return y, r

@@ -52,17 +52,25 @@ ssd_status cuda_status(cudaError_t e) {
 // before (a thread per rank, say) would otherwise reach the first launch
 // without a current context.
 ssd_status check_device() {
-    int dev = 0, major = 0, minor = 0;
+    constexpr int kMaxDevices = 64;
+    static std::atomic<int> known[kMaxDevices];  // 0 not asked yet, 1 this build's architecture, 2 another
+    int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) {
         cudaGetLastError();
         return SSD_ERR_UNSUPPORTED;
     }
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return SSD_ERR_UNSUPPORTED;
+    int k = dev >= 0 && dev < kMaxDevices ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (k == 0) {
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess) {
+            cudaGetLastError();
+            return SSD_ERR_UNSUPPORTED;
+        }
+        k = major == 10 && minor == 0 ? 1 : 2;
+        if (dev >= 0 && dev < kMaxDevices) known[dev].store(k, std::memory_order_relaxed);  // a race repeats the query
     }
-    return (major == 10 && minor == 0) ? SSD_OK : SSD_ERR_UNSUPPORTED;
+    return k == 1 ? SSD_OK : SSD_ERR_UNSUPPORTED;
 }
 
 }  // namespace ssd

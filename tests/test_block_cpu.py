@@ -82,15 +82,21 @@ def test_struct_sizes():
 
 
 def _change(p, **kw):
+    """Fields of a problem set; x_stride=(batch, token) and split=(a, b, c) set one field per element."""
     for k, v in kw.items():
-        if isinstance(v, (tuple, list)):
-            v = type(getattr(p, k))(*v)
-        setattr(p, k, v)
+        if k == "split":
+            p.split0, p.split1, p.split2 = v
+        elif k.endswith("_stride"):
+            setattr(p, k[:-6] + "batch_stride", v[0])
+            setattr(p, k[:-6] + "token_stride", v[1])
+        else:
+            assert k in dict(p._fields_)
+            setattr(p, k, v)
     return p
 
 
 def conv_problem(**kw):
-    return _change(block.ConvProblem(2, 64, 96, 4, 1, (64 * 96, 96), (64, 16, 16), BF16, 1), **kw)
+    return _change(block.ConvProblem(2, 64, 96, 4, 1, 64 * 96, 96, 64, 16, 16, BF16, 1), **kw)
 
 
 def conv(p, x=FAKE(0), weight=FAKE(1), bias=None, init=None, seq=None, out0=FAKE(2), out1=FAKE(3), out2=FAKE(4),
@@ -141,7 +147,7 @@ def test_conv_refuses_misaligned_overlapping_and_surplus_tensors():
 
 
 def selective_problem(**kw):
-    p = block.SelectiveProblem(2, 64, 96, 16, 2, 1, *[(64 * 96, 96)] * 3, *[(64 * 32, 32)] * 2, BF16, 1)
+    p = block.SelectiveProblem(2, 64, 96, 16, 2, 1, *[64 * 96, 96] * 3, *[64 * 32, 32] * 2, BF16, 1)
     return _change(p, **kw)
 
 
@@ -188,7 +194,7 @@ def test_selective_refuses_misaligned_and_overlapping_tensors():
 
 
 def norm_problem(**kw):
-    return _change(block.NormProblem(2, 64, 96, 1, (64 * 96, 96), (64 * 96, 96), BF16, F32, 1e-5, 1.0, 1), **kw)
+    return _change(block.NormProblem(2, 64, 96, 1, *[64 * 96, 96] * 2, BF16, F32, 1e-5, 1.0, 1), **kw)
 
 
 def gnorm(p, x=FAKE(0), z=FAKE(1), w=FAKE(2), out=FAKE(3)):
