@@ -26,22 +26,13 @@ namespace ssd {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-// 2^x, the hardware approximation (denormal results flushed to 0)
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // softplus(z) = max(z, 0) + log(1 + e), e = exp(-|z|) in [0, 1]. The logarithm
 // as 2 atanh(r), r = e / (2 + e) <= 1/3, by its power series: the first term left
 // out is r^17 / 17 < 5e-10 of r, and small e keep their relative accuracy, which
 // log(1 + e) taken directly would lose.
 __device__ __forceinline__ float softplus(float z) {
-    const float e = exp2_fast(-kLog2e * fabsf(z));
-    const float r = __fdividef(e, 2.f + e), q = r * r;
+    const float e = exp2_approx(-kLog2e * fabsf(z));
+    const float r = e * rcp_approx(2.f + e), q = r * r;
     float s = 1.f / 15.f;
     s = fmaf(s, q, 1.f / 13.f);
     s = fmaf(s, q, 1.f / 11.f);
@@ -51,22 +42,6 @@ __device__ __forceinline__ float softplus(float z) {
     s = fmaf(s, q, 1.f / 3.f);
     s = fmaf(s, q, 1.f);
     return fmaf(2.f * r, s, fmaxf(z, 0.f));
-}
-
-// Asynchronous copy of `bytes` bytes (2, 4, ... kBytes) to shared memory, zeros behind them.
-template <int kBytes>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
-    const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(bytes), "n"(kBytes)
-                     : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 
 constexpr int kStages = 3;  // slices of raw inputs in shared memory: two in flight behind the current one
@@ -349,7 +324,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             for (int j = 0; j < S2; ++j) {
 #pragma unroll
                 for (int m = 0; m < CH; ++m) {
-                    av[t][m][j] = make_float2(exp2_fast(d.v[2 * m] * A2[m][j].x), exp2_fast(d.v[2 * m] * A2[m][j].y));
+                    av[t][m][j] = make_float2(exp2_approx(d.v[2 * m] * A2[m][j].x), exp2_approx(d.v[2 * m] * A2[m][j].y));
                     hv[t][m][j] = make_float2(d.v[2 * m + 1] * Bt.v[2 * j], d.v[2 * m + 1] * Bt.v[2 * j + 1]);
                 }
             }
@@ -478,7 +453,7 @@ __global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const Sele
 #pragma unroll
         for (int j = 0; j < 16; ++j)
             if (n0 + j < N) {
-                const float e = exp2_fast(d * (A[n0 + j] * kLog2e));
+                const float e = exp2_approx(d * (A[n0 + j] * kLog2e));
                 const float v = fmaf(e, hv[j], du * to_f32(B[n0 + j]));
                 h[(int64_t)(n0 + j) * a.channels] = v;
                 y = fmaf(to_f32(C[n0 + j]), v, y);
