@@ -428,39 +428,88 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
 }
 
 constexpr int kStepThreads = 128;
+constexpr int kStepStates = 16;  // states of a thread in flight per row
 
-// One thread per (row, channel): its N states in and out, in batches of 16.
-template <typename T>
-__global__ void __launch_bounds__(kStepThreads) selective_step_kernel(const SelectiveArgs a, int blocks) {
-    const int b = blockIdx.x / blocks;
-    const int c = (blockIdx.x % blocks) * kStepThreads + threadIdx.x;
-    if (c >= a.channels) return;
-    const int N = a.dstate, g = c / (a.channels / a.ngroups);
-    const float uf = to_f32(static_cast<const T*>(a.u)[b * a.us_b + c]);
-    float d = to_f32(static_cast<const T*>(a.dt)[b * a.ds_b + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
-    if (a.softplus) d = softplus(d);
-    const float du = d * uf;
+// One token: a thread takes one channel of a batch row, kStepStates states at a
+// time; a CTA's channels lie in one group, whose B and C rows it keeps in shared
+// memory. Bound by the state's bytes, read and written once.
+// kVec: A's rows allow 16-byte loads; kWhole: N is a multiple of kStepStates.
+// Offsets within a row's state (at most 2^20 x 256 floats, 1 GB) are 32 bits from a
+// CTA-wide base: with 64-bit addresses per access their arithmetic was most of
+// the kernel's instructions.
+template <typename T, bool kVec, bool kWhole>
+__global__ void __launch_bounds__(kStepThreads, 5) selective_step_kernel(const SelectiveArgs a, int blocks_per_group) {
+    __shared__ float4 sm_b[kStepStates / 4], sm_c[kStepStates / 4];
+    const int N = a.dstate, per = a.channels / a.ngroups;
+    const int bg = blockIdx.x / blocks_per_group, b = bg / a.ngroups, g = bg % a.ngroups;
+    const int cg = (blockIdx.x % blocks_per_group) * kStepThreads + threadIdx.x;
+    const bool live = cg < per;
+    const int c = g * per + min(cg, per - 1);
     const T* B = static_cast<const T*>(a.B) + b * a.bs_b + g * N;
     const T* C = static_cast<const T*>(a.C) + b * a.cs_b + g * N;
-    float* h = a.final_states + (int64_t)b * N * a.channels + c;
-    const float* A = a.A + (int64_t)c * N;
-    float y = a.D ? a.D[c] * uf : 0.f;
-    for (int n0 = 0; n0 < N; n0 += 16) {
-        float hv[16];
+    char* hb = reinterpret_cast<char*>(a.final_states + (int64_t)b * N * a.channels);
+    const uint32_t step = 4u * (uint32_t)a.channels;
+    uint32_t off = 4u * (uint32_t)c;
+    const auto in = [&](int n) { return kWhole || n < N; };
+    float d = 0.f, du = 0.f, y = 0.f, zf = 0.f;
+    for (int n0 = 0; n0 < N; n0 += kStepStates) {
+        float hv[kStepStates], A2[kStepStates];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (n0 + j < N) hv[j] = h[(int64_t)(n0 + j) * a.channels];
+        for (int j = 0; j < kStepStates; ++j)
+            if (in(n0 + j)) hv[j] = __ldcs(reinterpret_cast<const float*>(hb + (off + j * step)));
+        const char* Ab = reinterpret_cast<const char*>(a.A);
+        const uint32_t aoff = 4u * ((uint32_t)c * (uint32_t)N + (uint32_t)n0);
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (n0 + j < N) {
-                const float e = exp2_approx(d * (A[n0 + j] * kLog2e));
-                const float v = fmaf(e, hv[j], du * to_f32(B[n0 + j]));
-                h[(int64_t)(n0 + j) * a.channels] = v;
-                y = fmaf(to_f32(C[n0 + j]), v, y);
+        for (int j = 0; j < kStepStates; j += kVec ? 4 : 1) {
+            using Q = Pack<float, kVec ? 4 : 1>;
+            if (in(n0 + j)) *reinterpret_cast<Q*>(A2 + j) = *reinterpret_cast<const Q*>(Ab + (aoff + 4u * j));
+        }
+        if (n0 == 0) {
+            const float uf = to_f32(static_cast<const T*>(a.u)[b * a.us_b + c]);
+            d = to_f32(static_cast<const T*>(a.dt)[b * a.ds_b + c]) + (a.dt_bias ? a.dt_bias[c] : 0.f);
+            if (a.z) zf = to_f32(static_cast<const T*>(a.z)[b * a.zs_b + c]);
+            y = a.D ? a.D[c] * uf : 0.f;
+            if (a.softplus) d = softplus(d);
+            du = d * uf;
+            d *= kLog2e;
+        } else {
+            __syncthreads();  // the states before are done with B and C
+        }
+        if (threadIdx.x < kStepStates) {
+            const int n = n0 + threadIdx.x;
+            reinterpret_cast<float*>(sm_b)[threadIdx.x] = n < N ? to_f32(B[n]) : 0.f;
+            reinterpret_cast<float*>(sm_c)[threadIdx.x] = n < N ? to_f32(C[n]) : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < kStepStates / 4; ++q) {
+            const float4 Bq = sm_b[q], Cq = sm_c[q];
+            const float Bv[4] = {Bq.x, Bq.y, Bq.z, Bq.w}, Cv[4] = {Cq.x, Cq.y, Cq.z, Cq.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int j = 4 * q + k;
+                if (in(n0 + j)) {
+                    const float v = fmaf(exp2_approx(d * A2[j]), hv[j], du * Bv[k]);
+                    if (live) __stcs(reinterpret_cast<float*>(hb + (off + j * step)), v);
+                    y = fmaf(Cv[k], v, y);
+                }
             }
+        }
+        off += kStepStates * step;
     }
-    if (a.z) y *= silu_for<T>(to_f32(static_cast<const T*>(a.z)[b * a.zs_b + c]));
-    static_cast<T*>(a.y)[(int64_t)b * a.channels + c] = from_f32<T>(y);
+    if (live)
+        static_cast<T*>(a.y)[(int64_t)b * a.channels + c] = from_f32<T>(a.z ? y * silu_for<T>(zf) : y);
+}
+
+template <typename T>
+cudaError_t run_step(const SelectiveArgs& a, cudaStream_t st) {
+    const int per = a.channels / a.ngroups, bpg = (per + kStepThreads - 1) / kStepThreads;
+    const bool vec = VectorRule(4).address(a.A).elements(a.dstate).multiple_of(16);
+    const unsigned grid = (unsigned)((int64_t)a.batch * a.ngroups * bpg);
+    const auto kernel = a.dstate % kStepStates == 0 ? (vec ? selective_step_kernel<T, true, true> : selective_step_kernel<T, false, true>)
+                                                    : (vec ? selective_step_kernel<T, true, false> : selective_step_kernel<T, false, false>);
+    kernel<<<grid, kStepThreads, 0, st>>>(a, bpg);
+    return cudaGetLastError();
 }
 
 template <typename T, typename Sh, int kMinCtas, bool kSeq, bool kCopy>
@@ -525,13 +574,7 @@ cudaError_t launch_selective_scan(const SelectiveArgs& a, ssd_dtype dt, cudaStre
 }
 
 cudaError_t launch_selective_step(const SelectiveArgs& a, ssd_dtype dt, cudaStream_t st) {
-    const int blocks = (a.channels + kStepThreads - 1) / kStepThreads;
-    const unsigned grid = (unsigned)((int64_t)a.batch * blocks);
-    if (dt == SSD_DTYPE_F32)
-        selective_step_kernel<float><<<grid, kStepThreads, 0, st>>>(a, blocks);
-    else
-        selective_step_kernel<__nv_bfloat16><<<grid, kStepThreads, 0, st>>>(a, blocks);
-    return cudaGetLastError();
+    return dt == SSD_DTYPE_F32 ? run_step<float>(a, st) : run_step<__nv_bfloat16>(a, st);
 }
 
 }  // namespace ssd
