@@ -20,6 +20,8 @@
 // Bound by the special-function unit (one exponential per (token, channel,
 // state)) and by shared memory's B, C and delta, read once per lane.
 
+#include <type_traits>
+
 #include "ssd_block.cuh"
 
 namespace ssd {
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     int tbytes[kCopy ? Sh::TR : 1];
     const T* bsrc[kCopy ? Sh::BR : 1];
     int64_t bstep[kCopy ? Sh::BR : 1];
+    int bbytes[kCopy ? Sh::BR : 1];
     T ru[kCopy ? 1 : OWN], rd[kCopy ? 1 : OWN], rz[kCopy ? 1 : OWN];
     if constexpr (kCopy) {
         constexpr int PT = Sh::ROW / Sh::TB, PB = 2 * NP / Sh::BV;
@@ -197,24 +200,22 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         for (int i = 0; i < Sh::BR; ++i) {  // copy v: token, B or C, states
             const int v = lane + 32 * i, t = v / PB, r = v % PB, n = r % (PB / 2) * Sh::BV;
             const int64_t step = r < PB / 2 ? a.bs_t : a.cs_t;
-            bstep[i] = n < N ? step * (K * L) : -1;
+            bstep[i] = step * (K * L);
+            bbytes[i] = n < N ? 16 : 0;
             bsrc[i] = (r < PB / 2 ? B : C) + (w * L + t) * step + (n < N ? n : 0);
         }
     }
-    const auto fetch = [&](int tw, int stage) {  // the slice that starts at token tw
+    // the slice that starts at token tw; full: it lies inside the row
+    const auto fetch = [&](int tw, int stage, auto full) {
         if constexpr (kCopy) {
             char* dst = sm_raw + stage + lane * Sh::TB;
             char* dst_bc = sm_raw + stage + 3 * L * Sh::ROW + lane * 16;
-            const bool full = tw + L <= a.seqlen;
 #pragma unroll
             for (int i = 0; i < Sh::TR; ++i) {
                 const int t = (lane + 32 * i) / (Sh::ROW / Sh::TB) % L;
                 if (tbytes[i] >= 0) {
-                    if (full)
-                        copy_async<Sh::TB>(dst + i * 32 * Sh::TB, tsrc[i], tbytes[i]);
-                    else
-                        copy_async<Sh::TB>(dst + i * 32 * Sh::TB, tw + t < a.seqlen ? tsrc[i] : u,
-                                           tw + t < a.seqlen ? tbytes[i] : 0);
+                    const bool in = full || tw + t < a.seqlen;
+                    copy_async<Sh::TB>(dst + i * 32 * Sh::TB, in ? tsrc[i] : u, in ? tbytes[i] : 0);
                     tsrc[i] += tstep[i];
                 }
             }
@@ -222,8 +223,8 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             for (int i = 0; i < Sh::BR; ++i) {
                 const int t = (lane + 32 * i) / (2 * NP / Sh::BV);
                 if (Sh::BN % 32 == 0 || lane + 32 * i < Sh::BN) {
-                    const bool in = (full || tw + t < a.seqlen) && bstep[i] >= 0;
-                    copy_async<16>(dst_bc + i * 512, in ? bsrc[i] : B, in ? 16 : 0);
+                    const bool in = full || tw + t < a.seqlen;
+                    copy_async<16>(dst_bc + i * 512, in ? bsrc[i] : B, in ? bbytes[i] : 0);
                     bsrc[i] += bstep[i];
                 }
             }
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             for (int i = 0; i < OWN; ++i) {
                 const int t = tw + tok(i), cg = min(cg0 + cl(i), per - 1);
                 ru[i] = rd[i] = rz[i] = from_f32<T>(0.f);
-                if (t < a.seqlen) {
+                if (full || t < a.seqlen) {
                     ru[i] = u[t * a.us_t + cg];
                     rd[i] = dt[t * a.ds_t + cg];
                     if (a.z) rz[i] = z[t * a.zs_t + cg];
@@ -242,14 +243,29 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         }
     };
 
-    fetch(w * L, 0);
-    if (kCopy) fetch((K + w) * L, Sh::RAW);
+    // hand a state on to the next warp
+    const int next = w == K - 1 ? 0 : w + 1;
+    const auto put_state = [&](const State& h) {
+#pragma unroll
+        for (int i = 0; i < CH * S / 4; ++i) {
+            const float2 lo = h[4 * i / S][4 * i % S / 2], hi = h[4 * i / S][4 * i % S / 2 + 1];
+            sm_next[i * 32] = make_float4(lo.x, lo.y, hi.x, hi.y);
+        }
+        asm volatile("barrier.arrive %0, 64;" ::"r"(next) : "memory");
+    };
+    fetch(w * L, 0, std::false_type());
+    if (kCopy) fetch((K + w) * L, Sh::RAW, std::false_type());
     int stage = 0;  // byte offset of the current raw stage
     T* y = static_cast<T*>(a.y) + (row0 + w * L + tok(0)) * a.channels + g * per + cg0 + cl(0);
-    const int tiles = (a.seqlen + K * L - 1) / (K * L);
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int tw = (tile * K + w) * L;
-        const bool past_end = tw + L > a.seqlen;
+    if (w == K - 1) {  // the state before the row, for warp 0's first slice
+        State h;
+        init_state(h, 0);
+        put_state(h);
+    }
+    // The slice that starts at token tw. full: it, and the slice fetched meanwhile, lie inside the row, and
+    // it is not the row's last one.
+    const auto slice = [&](int tw, auto full) {
+        const bool past_end = !full && tw + L > a.seqlen;
         // ---- this slice's (delta, delta u), B and C, in fp32 ----
         if (kCopy) copy_wait<1>();
         __syncwarp();
@@ -292,7 +308,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                             to_f32(e.v[k]), to_f32(e.v[k + 1]), to_f32(e.v[k + 2]), to_f32(e.v[k + 3]));
                 }
             }
-            fetch(tw + 2 * K * L, stage == 0 ? 2 * Sh::RAW : stage - Sh::RAW);
+            fetch(tw + 2 * K * L, stage == 0 ? 2 * Sh::RAW : stage - Sh::RAW, full);
             stage = stage == (kStages - 1) * Sh::RAW ? 0 : stage + Sh::RAW;
         } else {
             for (int i = lane; i < Sh::BC; i += 32) {
@@ -301,7 +317,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                 if (n < N && t < a.seqlen) v = to_f32(r < NP ? B[t * a.bs_t + n] : C[t * a.cs_t + n]);
                 sm_bc[i] = v;
             }
-            fetch(tw + K * L, 0);
+            fetch(tw + K * L, 0, full);
         }
         // sequences that start in this slice: lane i < L looks at token tw + i
         unsigned starts = 0u;
@@ -331,23 +347,12 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         }
         // ---- the recurrence: the state from the slice before, through this one, to the next ----
         State h;
-        if (w == 0 && tile == 0) {
-            if (kSeq) {
+        asm volatile("barrier.sync %0, 64;" ::"r"(w) : "memory");  // with the arrival of the warp before
 #pragma unroll
-                for (int m = 0; m < CH; ++m)
-#pragma unroll
-                    for (int j = 0; j < S2; ++j) h[m][j] = make_float2(0.f, 0.f);
-            } else {
-                init_state(h, 0);
-            }
-        } else {
-            asm volatile("barrier.sync %0, 64;" ::"r"(w) : "memory");  // with the arrival of warp w - 1
-#pragma unroll
-            for (int i = 0; i < CH * S / 4; ++i) {
-                const float4 q = sm_state[i * 32];
-                h[4 * i / S][4 * i % S / 2] = make_float2(q.x, q.y);
-                h[4 * i / S][4 * i % S / 2 + 1] = make_float2(q.z, q.w);
-            }
+        for (int i = 0; i < CH * S / 4; ++i) {
+            const float4 q = sm_state[i * 32];
+            h[4 * i / S][4 * i % S / 2] = make_float2(q.x, q.y);
+            h[4 * i / S][4 * i % S / 2 + 1] = make_float2(q.z, q.w);
         }
 #pragma unroll
         for (int t = 0; t < L; ++t) {
@@ -364,16 +369,8 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
 #pragma unroll
                 for (int j = 0; j < S2; ++j) h[m][j] = hv[t][m][j] = __ffma2_rn(av[t][m][j], h[m][j], hv[t][m][j]);
         }
-        if (w < K - 1 || tile < tiles - 1) {
-            const int next = w == K - 1 ? 0 : w + 1;
-#pragma unroll
-            for (int i = 0; i < CH * S / 4; ++i) {
-                const float2 lo = h[4 * i / S][4 * i % S / 2], hi = h[4 * i / S][4 * i % S / 2 + 1];
-                sm_next[i * 32] = make_float4(lo.x, lo.y, hi.x, hi.y);
-            }
-            asm volatile("barrier.arrive %0, 64;" ::"r"(next) : "memory");
-        }
-        if (a.final_states && tw < a.seqlen && tw + L >= a.seqlen) {  // this slice has the row's last token
+        if (full || w < K - 1 || tw + L < a.seqlen) put_state(h);  // the row's last tile ends the chain
+        if (!full && a.final_states && tw < a.seqlen && tw + L >= a.seqlen) {  // this slice has the row's last token
             const int s = kSeq ? __shfl_sync(0xffffffffu, id, a.seqlen - 1 - tw) : 0;
             write_state(h, s);
             keep(s + 1, a.nseq);
@@ -424,7 +421,12 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             }
         }
         y += (int64_t)(K * L) * a.channels;
-    }
+    };
+    const int tiles = (a.seqlen + K * L - 1) / (K * L);
+    // whole: the tiles whose fetches, two tiles ahead at most, lie inside the row
+    const int whole = max(0, min(a.seqlen / (K * L) - 2, tiles - 1));
+    for (int tile = 0; tile < whole; ++tile) slice((tile * K + w) * L, std::true_type());
+    for (int tile = whole; tile < tiles; ++tile) slice((tile * K + w) * L, std::false_type());
 }
 
 constexpr int kStepThreads = 128;
