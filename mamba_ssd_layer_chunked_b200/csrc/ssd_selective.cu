@@ -66,12 +66,14 @@ struct ScanShape {
     static constexpr int BV = 16 / E;                          // B, C elements per copy
     static constexpr int BN = L * 2 * NP / BV;                 // such copies per slice
     static constexpr int BR = (BN + 31) / 32;                  // and per lane
-    static constexpr bool kCanCopy = TB >= 4 && NP >= BV && BR <= 4;
-    static constexpr int VW = CH == 2 && OWN % 2 == 0 ? 2 : 1; // owned channels that lie side by side
+    static constexpr bool kCanCopy = TB >= 4 && NP >= BV && BR <= 8;
     static constexpr int PAIR = L * CPW * 2;                   // floats: (delta, delta u) per token and channel
     static constexpr int BC = L * 2 * NP;                      // floats: B and C of the slice
+    static constexpr int NB = BC / 32;                         // of those, a lane's share
     static constexpr int STATE = CH * S * 32;                  // floats: a state handed on
-    static constexpr int RAW = 3 * L * ROW + BC * E;           // bytes of a raw stage
+    static constexpr int TOKENS = (3 * L * ROW + 15) / 16 * 16; // bytes of u, dt, z in a raw stage
+    static constexpr int RAW = TOKENS + BC * E;                // bytes of a raw stage
+    static_assert(PAIR % 4 == 0 && BC % 4 == 0 && STATE % 4 == 0 && BC * E % 16 == 0, "16-byte parts");
     static constexpr int smem(bool copies) { return K * (PAIR + BC + STATE) * 4 + (copies ? K * kStages * RAW : 0); }
 };
 
@@ -84,7 +86,7 @@ template <typename T, typename Sh, int kMinCtas, bool kSeq, bool kCopy>
 __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(const SelectiveArgs a,
                                                                               int units_per_group) {
     constexpr int CH = Sh::CH, S = Sh::S, L = Sh::L, K = Sh::K, COLS = Sh::COLS, CPW = Sh::CPW, NP = Sh::NP;
-    constexpr int S2 = S / 2, OWN = Sh::OWN, VW = Sh::VW;
+    constexpr int S2 = S / 2, OWN = Sh::OWN;
     extern __shared__ float4 smem4[];
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int col = lane % COLS, ns = lane / COLS, N = a.dstate;
@@ -183,6 +185,14 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     int64_t bstep[kCopy ? Sh::BR : 1];
     int bbytes[kCopy ? Sh::BR : 1];
     T ru[kCopy ? 1 : OWN], rd[kCopy ? 1 : OWN], rz[kCopy ? 1 : OWN];
+    T rbc[kCopy ? 1 : Sh::NB];
+    // element lane + 32 i of the slice's B and C
+    const auto bc_element = [&](int tw, int i, auto full) {
+        const int v = lane + 32 * i, r = v % (2 * NP), n = r % NP, t = tw + v / (2 * NP);
+        T e = from_f32<T>(0.f);
+        if (n < N && (full || t < a.seqlen)) e = r < NP ? B[t * a.bs_t + n] : C[t * a.cs_t + n];
+        return e;
+    };
     if constexpr (kCopy) {
         constexpr int PT = Sh::ROW / Sh::TB, PB = 2 * NP / Sh::BV;
 #pragma unroll
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     const auto fetch = [&](int tw, int stage, auto full) {
         if constexpr (kCopy) {
             char* dst = sm_raw + stage + lane * Sh::TB;
-            char* dst_bc = sm_raw + stage + 3 * L * Sh::ROW + lane * 16;
+            char* dst_bc = sm_raw + stage + Sh::TOKENS + lane * 16;
 #pragma unroll
             for (int i = 0; i < Sh::TR; ++i) {
                 const int t = (lane + 32 * i) / (Sh::ROW / Sh::TB) % L;
@@ -240,6 +250,8 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                     if (a.z) rz[i] = z[t * a.zs_t + cg];
                 }
             }
+#pragma unroll
+            for (int i = 0; i < Sh::NB; ++i) rbc[i] = bc_element(tw, i, full);
         }
     };
 
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             const float2 lo = h[4 * i / S][4 * i % S / 2], hi = h[4 * i / S][4 * i % S / 2 + 1];
             sm_next[i * 32] = make_float4(lo.x, lo.y, hi.x, hi.y);
         }
-        asm volatile("barrier.arrive %0, 64;" ::"r"(next) : "memory");
+        asm volatile("bar.arrive %0, 64;" ::"r"(next) : "memory");
     };
     fetch(w * L, 0, std::false_type());
     if (kCopy) fetch((K + w) * L, Sh::RAW, std::false_type());
@@ -262,38 +274,35 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         init_state(h, 0);
         put_state(h);
     }
+    // What a slice is prepared to, carried from one turn of the loop to the next: the compiler then cannot
+    // move the exponentials behind the wait for the state, where they would delay every warp of the CTA.
+    float2 av[L][CH][S2], hv[L][CH][S2];  // a and v
+    float skip[OWN], gate[OWN];
+    unsigned starts = 0u;  // sequences that start in the slice: bit t for token t
+    int id = 0, id_before = -1;
     // The slice that starts at token tw. full: it, and the slice fetched meanwhile, lie inside the row, and
     // it is not the row's last one.
-    const auto slice = [&](int tw, auto full) {
+    const auto prepare = [&](int tw, auto full) {
         const bool past_end = !full && tw + L > a.seqlen;
         // ---- this slice's (delta, delta u), B and C, in fp32 ----
         if (kCopy) copy_wait<1>();
         __syncwarp();
-        const char* raw = sm_raw + stage;
-        float skip[OWN], gate[OWN];
+        [[maybe_unused]] const char* raw = sm_raw + stage;
 #pragma unroll
-        for (int i = 0; i < OWN; i += VW) {
-            Pack<T, VW> ue, de, ze;
+        for (int i = 0; i < OWN; ++i) {
+            float uf, d, zf;
             if constexpr (kCopy) {
-                const auto* e = reinterpret_cast<const Pack<T, VW>*>(raw + (tok(i) * CPW + cl(i)) * Sh::E);
-                ue = e[0], de = e[L * CPW / VW], ze = e[2 * L * CPW / VW];
+                const T* e = reinterpret_cast<const T*>(raw) + tok(i) * CPW + cl(i);
+                uf = to_f32(e[0]), d = to_f32(e[L * CPW]), zf = to_f32(e[2 * L * CPW]);
             } else {
-#pragma unroll
-                for (int k = 0; k < VW; ++k) ue.v[k] = ru[i + k], de.v[k] = rd[i + k], ze.v[k] = rz[i + k];
+                uf = to_f32(ru[i]), d = to_f32(rd[i]), zf = to_f32(rz[i]);
             }
-            Pack<float, 2 * VW> pair;
-#pragma unroll
-            for (int k = 0; k < VW; ++k) {
-                const float uf = to_f32(ue.v[k]);
-                float d = to_f32(de.v[k]) + bias[i + k];
-                if (a.softplus) d = softplus(d);
-                if (past_end && tw + tok(i) >= a.seqlen) d = 0.f;  // a = 1 and no input
-                skip[i + k] = D[i + k] * uf;
-                gate[i + k] = a.z ? silu_for<T>(to_f32(ze.v[k])) : 1.f;
-                pair.v[2 * k] = d;
-                pair.v[2 * k + 1] = d * uf;
-            }
-            *reinterpret_cast<Pack<float, 2 * VW>*>(sm_pair + (tok(i) * CPW + cl(i)) * 2) = pair;
+            d += bias[i];
+            if (a.softplus) d = softplus(d);
+            if (past_end && tw + tok(i) >= a.seqlen) d = 0.f;  // a = 1 and no input
+            skip[i] = D[i] * uf;
+            gate[i] = a.z ? silu_for<T>(zf) : 1.f;
+            *reinterpret_cast<float2*>(sm_pair + (tok(i) * CPW + cl(i)) * 2) = make_float2(d, d * uf);
         }
         if constexpr (kCopy) {
 #pragma unroll
@@ -301,7 +310,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                 const int v = lane + 32 * i;
                 if (Sh::BN % 32 == 0 || v < Sh::BN) {
                     const Pack<T, Sh::BV> e =
-                        *reinterpret_cast<const Pack<T, Sh::BV>*>(raw + 3 * L * Sh::ROW + v * 16);
+                        *reinterpret_cast<const Pack<T, Sh::BV>*>(raw + Sh::TOKENS + v * 16);
 #pragma unroll
                     for (int k = 0; k < Sh::BV; k += 4)
                         *reinterpret_cast<float4*>(sm_bc + v * Sh::BV + k) = make_float4(
@@ -311,26 +320,19 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             fetch(tw + 2 * K * L, stage == 0 ? 2 * Sh::RAW : stage - Sh::RAW, full);
             stage = stage == (kStages - 1) * Sh::RAW ? 0 : stage + Sh::RAW;
         } else {
-            for (int i = lane; i < Sh::BC; i += 32) {
-                const int r = i % (2 * NP), n = r % NP, t = tw + i / (2 * NP);
-                float v = 0.f;
-                if (n < N && t < a.seqlen) v = to_f32(r < NP ? B[t * a.bs_t + n] : C[t * a.cs_t + n]);
-                sm_bc[i] = v;
-            }
+#pragma unroll
+            for (int i = 0; i < Sh::NB; ++i) sm_bc[lane + 32 * i] = to_f32(rbc[i]);
             fetch(tw + K * L, 0, full);
         }
-        // sequences that start in this slice: lane i < L looks at token tw + i
-        unsigned starts = 0u;
-        int id = 0, id_before = -1;
-        if (kSeq) {
+        if (kSeq) {  // lane i < L looks at token tw + i
             const int t = min(tw + lane % L, a.seqlen - 1);
             id = seq_at(a.seq_idx, row0, t, a.nseq);
+            id_before = -1;
             if (t > 0) id_before = seq_at(a.seq_idx, row0, t - 1, a.nseq);
             starts = __ballot_sync(0xffffffffu, lane < L && tw + lane < a.seqlen && (t == 0 || id != id_before));
         }
         __syncwarp();
         // ---- a and v of the slice ----
-        float2 av[L][CH][S2], hv[L][CH][S2];
 #pragma unroll
         for (int t = 0; t < L; ++t) {
             const Pack<float, 2 * CH> d = *reinterpret_cast<const Pack<float, 2 * CH>*>(
@@ -345,9 +347,13 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                 }
             }
         }
+    };
+    // The recurrence through the prepared slice, and its read-out.
+    const auto finish = [&](int tw, auto full) {
+        const bool past_end = !full && tw + L > a.seqlen;
         // ---- the recurrence: the state from the slice before, through this one, to the next ----
         State h;
-        asm volatile("barrier.sync %0, 64;" ::"r"(w) : "memory");  // with the arrival of the warp before
+        asm volatile("bar.sync %0, 64;" ::"r"(w) : "memory");  // with the arrival of the warp before
 #pragma unroll
         for (int i = 0; i < CH * S / 4; ++i) {
             const float4 q = sm_state[i * 32];
@@ -406,27 +412,26 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             }
         }
 #pragma unroll
-        for (int i = 0; i < OWN; i += VW) {
-            T* yi = y + (int64_t)(tok(i) - tok(0)) * a.channels + (cl(i) - cl(0));
-            Pack<T, VW> v;
-#pragma unroll
-            for (int k = 0; k < VW; ++k) v.v[k] = from_f32<T>((out[i + k] + skip[i + k]) * gate[i + k]);
-            if (past_end && tw + tok(i) >= a.seqlen) continue;
-            if (kCopy) {  // rows of whole 16-byte parts: a pair of channels is inside or outside as one
-                if (mine[i]) *reinterpret_cast<Pack<T, VW>*>(yi) = v;
-            } else {
-#pragma unroll
-                for (int k = 0; k < VW; ++k)
-                    if (mine[i + k]) yi[k] = v.v[k];
-            }
+        for (int i = 0; i < OWN; ++i) {
+            if (!mine[i] || (past_end && tw + tok(i) >= a.seqlen)) continue;
+            y[(int64_t)(tok(i) - tok(0)) * a.channels + (cl(i) - cl(0))] = from_f32<T>((out[i] + skip[i]) * gate[i]);
         }
         y += (int64_t)(K * L) * a.channels;
     };
     const int tiles = (a.seqlen + K * L - 1) / (K * L);
+    const int first_token = w * L, step = K * L;
     // whole: the tiles whose fetches, two tiles ahead at most, lie inside the row
-    const int whole = max(0, min(a.seqlen / (K * L) - 2, tiles - 1));
-    for (int tile = 0; tile < whole; ++tile) slice((tile * K + w) * L, std::true_type());
-    for (int tile = whole; tile < tiles; ++tile) slice((tile * K + w) * L, std::false_type());
+    const int whole = max(0, min(a.seqlen / step - 2, tiles - 1));
+    prepare(first_token, std::false_type());
+    int tile = 0;
+    for (; tile + 1 < whole; ++tile) {
+        finish(first_token + tile * step, std::true_type());
+        prepare(first_token + (tile + 1) * step, std::true_type());
+    }
+    for (; tile < tiles; ++tile) {
+        finish(first_token + tile * step, std::false_type());
+        if (tile + 1 < tiles) prepare(first_token + (tile + 1) * step, std::false_type());
+    }
 }
 
 constexpr int kStepThreads = 128;
@@ -536,7 +541,7 @@ cudaError_t run_scan(const SelectiveArgs& a, cudaStream_t st) {
         VectorRule tok(sizeof(T)), bc(sizeof(T));
         tok.address(a.u).address(a.dt).elements(a.us_b).elements(a.us_t).elements(a.ds_b).elements(a.ds_t);
         if (a.z) tok.address(a.z).elements(a.zs_b).elements(a.zs_t);
-        tok.address(a.y).elements(a.channels / a.ngroups);
+        tok.elements(a.channels / a.ngroups);
         bc.address(a.B).address(a.C).elements(a.bs_b).elements(a.bs_t).elements(a.cs_b).elements(a.cs_t);
         bc.elements(a.dstate);
         if (tok.multiple_of(Sh::TB) && bc.multiple_of(16))
@@ -547,16 +552,22 @@ cudaError_t run_scan(const SelectiveArgs& a, cudaStream_t st) {
                      : start_scan<T, Sh, kMinCtas, false, false>(a, st);
 }
 
-constexpr int64_t kManyCtas = 2 * 148;  // CTAs of 4 warps that keep every SM busy
-
+// LN lanes hold a channel's states. Up to 32 states: one channel per lane, 8 tokens
+// per slice; two CTAs of 8 warps per SM, or one of 16 while there are no more CTAs
+// than SMs. More states: two channels per lane, which halves the reads of B and C
+// (N 64, 1024 tokens x 5120 channels: 202 us against 287), and slices of 4.
 template <typename T, int LN>
 cudaError_t scan_by_size(const SelectiveArgs& a, cudaStream_t st) {
-    const int64_t per = a.channels / a.ngroups, rows = (int64_t)a.batch * a.ngroups;
-    const int64_t units = rows * ((per * LN + 63) / 64);  // CTAs with two channels per lane
-    if (units >= kManyCtas) return run_scan<T, ScanShape<T, 2, 4, LN, 4, 4>, 4>(a, st);
-    if (units * 2 >= kManyCtas) return run_scan<T, ScanShape<T, 1, 4, LN, 8, 4>, 5>(a, st);
-    if constexpr (LN <= 16) return run_scan<T, ScanShape<T, 1, 4, LN, 8, 16>, 1>(a, st);
-    return run_scan<T, ScanShape<T, 1, 4, LN, 8, 8>, 1>(a, st);
+    constexpr int kChannels = 32 / LN * (LN <= 8 ? 1 : 2);  // per CTA
+    const int64_t per = a.channels / a.ngroups;
+    const int64_t ctas = (int64_t)a.batch * a.ngroups * ((per + kChannels - 1) / kChannels);
+    if constexpr (LN <= 8) {
+        if (ctas <= 148) return run_scan<T, ScanShape<T, 1, 4, LN, 8, 16>, 1>(a, st);
+        return run_scan<T, ScanShape<T, 1, 4, LN, 8, 8>, 2>(a, st);
+    } else {
+        if (ctas <= 2 * 148) return run_scan<T, ScanShape<T, 2, 4, LN, 4, 8>, 2>(a, st);
+        return run_scan<T, ScanShape<T, 2, 4, LN, 4, 4>, 4>(a, st);
+    }
 }
 
 template <typename T>
@@ -566,7 +577,7 @@ cudaError_t scan_by_states(const SelectiveArgs& a, cudaStream_t st) {
     if (a.dstate <= 32) return scan_by_size<T, 8>(a, st);
     if (a.dstate <= 64) return scan_by_size<T, 16>(a, st);
     if (a.dstate <= 128) return scan_by_size<T, 32>(a, st);
-    return run_scan<T, ScanShape<T, 1, 8, 32, 4, 4>, 2>(a, st);
+    return run_scan<T, ScanShape<T, 2, 8, 32, 2, 8>, 2>(a, st);
 }
 
 }  // namespace

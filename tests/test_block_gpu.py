@@ -160,6 +160,13 @@ SCAN = {
     "many_states": (1, 20, 36, 64, 1, "f32", None, 1, (0, 0), True, False, True, True),
     "odd_states": (2, 31, 40, 67, 1, "bf16", None, 1, (0, 0), True, True, True, True),
     "most_states": (1, 9, 10, 256, 1, "f32", None, 1, (0, 0), True, True, True, True),
+    # 16-byte and narrower asynchronous copies of every shape: aligned rows, full tiles
+    "most_states_bf16": (1, 150, 10, 256, 1, "bf16", None, 1, (0, 0), True, True, True, True),
+    "states_128_bf16": (1, 150, 12, 128, 1, "bf16", None, 1, (0, 0), True, True, True, True),
+    "states_128_f32": (1, 150, 12, 128, 1, "f32", [[70, 80]], 2, (0, 0), True, True, True, True),
+    "states_64_bf16": (1, 150, 20, 64, 1, "bf16", [[70, 80]], 2, (0, 0), True, True, True, True),
+    "states_32_bf16": (1, 150, 20, 32, 1, "bf16", None, 1, (0, 0), True, True, True, True),
+    "states_8_f32": (1, 300, 64, 8, 1, "f32", None, 1, (0, 0), True, True, True, True),
     "packed": (2, 100, 48, 16, 1, "bf16", [[40, 60], [1, 99]], 2, (16, 0), True, True, True, True),
     "packed_short": (2, 40, 34, 16, 2, "f32", [[1, 1, 1, 2, 3, 32], [8, 8, 8, 7, 1, 8]], 6, (0, 0), True, True, True,
                      True),
