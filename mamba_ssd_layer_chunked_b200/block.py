@@ -81,6 +81,9 @@ def _need(t: Optional[torch.Tensor], name: str, shape, dtype, device, dense=True
     """The address of t after checking it (None for an absent tensor)."""
     if t is None:
         return None
+    if (t.dtype is dtype and t.shape == shape and t.device == device
+            and (t.is_contiguous() or (not dense and t.stride(-1) == 1))):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}, not {t.dtype}")
     if t.shape != shape:
@@ -115,6 +118,11 @@ def _run_on(x: torch.Tensor, stream):
     return torch.cuda.stream(stream)
 
 
+def _like(x: torch.Tensor) -> torch.Tensor:
+    """A dense tensor of x's shape and type."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
+
+
 def _nseq(seq_idx, nseq) -> int:
     if nseq is None:
         if seq_idx is not None:
@@ -141,7 +149,7 @@ def _split(channels: int, splits: Optional[Sequence[int]]):
 def _outputs(lead, split, x, out, as_tuple):
     """The outputs' tensors (allocated, or checked) and their three addresses."""
     if out is None:
-        outs = [x.new_empty((*lead, n)) for n in split if n]
+        outs = [x.new_empty((*lead, n)) for n in split if n] if as_tuple else [_like(x)]
         ptrs = [o.data_ptr() for o in outs]
     else:
         outs = tuple(out) if as_tuple else (out,)
@@ -278,8 +286,8 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     initp = _need(init_states, "init_states", states, torch.float32, device)
     idsp = _need(seq_idx, "seq_idx", (b, T), torch.int32, device)
     p = ctypes.byref(SelectiveProblem(b, T, ch, N, G, nseq, *strides, dtype, 1 if dt_softplus else 0))
-    y = u.new_empty(u.shape) if out is None else out
-    yp = _need(y, "out", u.shape, u.dtype, device)
+    y = _like(u) if out is None else out
+    yp = y.data_ptr() if out is None else _need(y, "out", u.shape, u.dtype, device)
     final, finp = None, None
     if return_final_states:
         final = u.new_empty(states, dtype=torch.float32) if final_out is None else final_out
@@ -313,8 +321,8 @@ def selective_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     b, device = u.shape[0], u.device
     sp = _need(state, "state", (b, N, ch), torch.float32, device)
     p = SelectiveProblem(b, 1, ch, N, G, 1, *strides, dtype, 1 if dt_softplus else 0)
-    y = u.new_empty(u.shape) if out is None else out
-    yp = _need(y, "out", u.shape, u.dtype, device)
+    y = _like(u) if out is None else out
+    yp = y.data_ptr() if out is None else _need(y, "out", u.shape, u.dtype, device)
     _ssd._check(_fn.ssd_selective_step(ctypes.byref(p), *ptrs, sp, yp, _raw_stream(device.index)),
                 "ssd_selective_step")
     return y
@@ -349,8 +357,8 @@ def gated_norm(x: torch.Tensor, weight: torch.Tensor, z: Optional[torch.Tensor] 
     wp = _need(weight, "weight", (ch,), torch.float32, device)
     code = _dtype(x, "x")
     p = NormProblem(b, T, ch, int(ngroups), xs0, xs1, *zs, code, code, eps, 1.0, 1 if gate_first else 0)
-    y = x.new_empty(shape) if out is None else out
-    yp = _need(y, "out", shape, dtype, device)
+    y = _like(x) if out is None else out
+    yp = y.data_ptr() if out is None else _need(y, "out", shape, dtype, device)
     _ssd._check(_fn.ssd_gated_norm(ctypes.byref(p), xp, zp, wp, yp, _raw_stream(device.index)), "ssd_gated_norm")
     return y
 
@@ -383,8 +391,12 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     if per_channel:
         sp = _need(scale, "scale", (ch,), torch.float32, device)
     p = NormProblem(b, T, ch, 1, xs0, xs1, *rs, code, _DTYPES[rdt], eps, 1.0 if per_channel else scale, 0)
-    y = x.new_empty(shape) if out is None else out
-    r = x.new_empty(shape, dtype=rdt) if residual_out is None else residual_out
-    yp, rop = _need(y, "out", shape, dtype, device), _need(r, "residual_out", shape, rdt, device)
+    y = _like(x) if out is None else out
+    yp = y.data_ptr() if out is None else _need(y, "out", shape, dtype, device)
+    if residual_out is not None:
+        r = residual_out
+    else:
+        r = _like(residual) if residual is not None else x.new_empty(shape, dtype=rdt)
+    rop = r.data_ptr() if residual_out is None else _need(r, "residual_out", shape, rdt, device)
     _ssd._check(_fn.ssd_add_norm(ctypes.byref(p), xp, rp, wp, sp, yp, rop, _raw_stream(device.index)), "ssd_add_norm")
     return y, r
