@@ -87,6 +87,10 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                                                                               int units_per_group) {
     constexpr int CH = Sh::CH, S = Sh::S, L = Sh::L, K = Sh::K, COLS = Sh::COLS, CPW = Sh::CPW, NP = Sh::NP;
     constexpr int S2 = S / 2, OWN = Sh::OWN;
+    // bf16 B and C of many states are read where the copies put them: every lane of a column converts its own,
+    // but shared memory moves half the bytes and no staged fp32 copy is written (N 64: 199 -> 173 us, N 128: 256 ->
+    // 188 us per 5120 channels and 1024, 512 tokens; N 16 the other way, 209 -> 224 us for 4096 tokens).
+    constexpr bool kRawBC = kCopy && sizeof(T) == 2 && NP >= 32;
     extern __shared__ float4 smem4[];
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int col = lane % COLS, ns = lane / COLS, N = a.dstate;
@@ -278,6 +282,15 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     // move the exponentials behind the wait for the state, where they would delay every warp of the CTA.
     float2 av[L][CH][S2], hv[L][CH][S2];  // a and v
     float skip[OWN], gate[OWN];
+    [[maybe_unused]] const char* bc_raw = sm_raw;  // the slice's B and C as copied
+    // the lane's states of token t's B (which = 0) or C (1)
+    const auto load_bc = [&](int t, int which, float (&f)[S]) {
+        const int i = t * 2 * NP + which * NP + ns * S;
+        if constexpr (kRawBC)
+            unpack(*reinterpret_cast<const Pack<T, S>*>(bc_raw + i * Sh::E), f);
+        else
+            unpack(*reinterpret_cast<const Pack<float, S>*>(sm_bc + i), f);
+    };
     unsigned starts = 0u;  // sequences that start in the slice: bit t for token t
     int id = 0, id_before = -1;
     // The slice that starts at token tw. full: it, and the slice fetched meanwhile, lie inside the row, and
@@ -304,9 +317,10 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             gate[i] = a.z ? silu_for<T>(zf) : 1.f;
             *reinterpret_cast<float2*>(sm_pair + (tok(i) * CPW + cl(i)) * 2) = make_float2(d, d * uf);
         }
+        bc_raw = raw + Sh::TOKENS;
         if constexpr (kCopy) {
 #pragma unroll
-            for (int i = 0; i < Sh::BR; ++i) {
+            for (int i = 0; i < (kRawBC ? 0 : Sh::BR); ++i) {
                 const int v = lane + 32 * i;
                 if (Sh::BN % 32 == 0 || v < Sh::BN) {
                     const Pack<T, Sh::BV> e =
@@ -337,13 +351,14 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         for (int t = 0; t < L; ++t) {
             const Pack<float, 2 * CH> d = *reinterpret_cast<const Pack<float, 2 * CH>*>(
                 sm_pair + (t * CPW + col * CH) * 2);  // delta, delta u of each channel
-            const Pack<float, S> Bt = *reinterpret_cast<const Pack<float, S>*>(sm_bc + t * 2 * NP + ns * S);
+            float Bt[S];
+            load_bc(t, 0, Bt);
 #pragma unroll
             for (int j = 0; j < S2; ++j) {
 #pragma unroll
                 for (int m = 0; m < CH; ++m) {
                     av[t][m][j] = make_float2(exp2_approx(d.v[2 * m] * A2[m][j].x), exp2_approx(d.v[2 * m] * A2[m][j].y));
-                    hv[t][m][j] = make_float2(d.v[2 * m + 1] * Bt.v[2 * j], d.v[2 * m + 1] * Bt.v[2 * j + 1]);
+                    hv[t][m][j] = make_float2(d.v[2 * m + 1] * Bt[2 * j], d.v[2 * m + 1] * Bt[2 * j + 1]);
                 }
             }
         }
@@ -385,11 +400,12 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         float out[Sh::OUTS];
 #pragma unroll
         for (int t = 0; t < L; ++t) {
-            const Pack<float, S> Ct = *reinterpret_cast<const Pack<float, S>*>(sm_bc + t * 2 * NP + NP + ns * S);
+            float Ct[S];
+            load_bc(t, 1, Ct);
             float2 acc[CH];
 #pragma unroll
             for (int j = 0; j < S2; ++j) {
-                const float2 Cj = make_float2(Ct.v[2 * j], Ct.v[2 * j + 1]);
+                const float2 Cj = make_float2(Ct[2 * j], Ct[2 * j + 1]);
 #pragma unroll
                 for (int m = 0; m < CH; ++m)
                     acc[m] = j == 0 ? __fmul2_rn(Cj, hv[t][m][j]) : __ffma2_rn(Cj, hv[t][m][j], acc[m]);
