@@ -438,8 +438,9 @@ ssd_status ssd_decode_step(const ssd_problem* p, const void* x, const float* log
  *    SSD_ERR_INVALID_ARG (in-place state buffers apart); where an input is
  *    strided, what lies between its rows counts as part of it.
  *  - Sums, statistics and states are fp32; each output is rounded once.
- *  - batch * seqlen <= 2^31 - 1, channels <= 2^20, nseq <= 2^24, else
- *    SSD_ERR_UNSUPPORTED. */
+ *  - batch * seqlen <= 2^31 - 1, seqlen <= 2^30, channels <= 2^20, nseq <= 2^24,
+ *    strides <= 2^40, else SSD_ERR_UNSUPPORTED. No workspace, no backward pass
+ *    (the library has none of ssd_fwd either). */
 
 typedef enum {
     SSD_ACT_NONE = 0,
@@ -512,15 +513,11 @@ typedef struct {
  *   init_states   [batch, nseq, N, channels]         fp32 or NULL (= 0)
  *   seq_idx       [batch, seqlen]                    int32 or NULL (one sequence)
  *   y             [batch, seqlen, channels]          dtype, out
- *   final_states  [batch, nseq, N, channels]         fp32, out, or NULL
- *   workspace     >= ssd_selective_scan_workspace_bytes(p) bytes, 16-byte aligned
- *                 (may be NULL when that is 0); contents are ignored and
- *                 overwritten, and calls that may overlap need one each */
-size_t ssd_selective_scan_workspace_bytes(const ssd_selective_problem* p);  /* (size_t)-1 on invalid p */
+ *   final_states  [batch, nseq, N, channels]         fp32, out, or NULL */
 ssd_status ssd_selective_scan(const ssd_selective_problem* p, const void* u, const void* dt, const float* A,
                               const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
                               const float* init_states, const int32_t* seq_idx, void* y, float* final_states,
-                              void* workspace, size_t workspace_bytes, void* stream);
+                              void* stream);
 
 /* ssd_selective_step: the same for one token of every batch row, with the state
  * updated in place. seqlen, nseq and the token strides are not read.

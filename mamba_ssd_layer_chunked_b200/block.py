@@ -4,9 +4,9 @@ and the norms of a block. Argument marshalling only, as in ssd.py.
 
 Activations may be slices of a projection's output: their last dimension is
 contiguous, the others may have any stride. Every call runs on the device of its
-tensors and on that device's current torch stream, or on ``stream``; outputs and
-workspaces are allocated on the stream the call runs on. Inputs must be ready on
-that stream.
+tensors and on that device's current torch stream, or on ``stream``; outputs are
+allocated on the stream the call runs on. Inputs must be ready on that stream;
+their memory is kept until it is done with them.
 """
 from __future__ import annotations
 
@@ -20,7 +20,6 @@ from . import ssd as _ssd
 _DTYPES = {torch.float32: _ssd.SSD_DTYPE_F32, torch.bfloat16: _ssd.SSD_DTYPE_BF16}
 _ACTIVATIONS = {None: 0, "none": 0, "silu": 1}
 _i64 = ctypes.c_int64
-_INVALID_SIZE = ctypes.c_size_t(-1).value
 _fn = None  # the loaded library
 
 
@@ -59,8 +58,7 @@ def declare(lib):
     for name, argtypes, restype in (
             ("ssd_causal_conv", [P(ConvProblem)] + [vp] * 10, ctypes.c_int),
             ("ssd_conv_step", [P(ConvProblem)] + [vp] * 8, ctypes.c_int),
-            ("ssd_selective_scan_workspace_bytes", [P(SelectiveProblem)], ctypes.c_size_t),
-            ("ssd_selective_scan", [P(SelectiveProblem)] + [vp] * 13 + [ctypes.c_size_t, vp], ctypes.c_int),
+            ("ssd_selective_scan", [P(SelectiveProblem)] + [vp] * 13, ctypes.c_int),
             ("ssd_selective_step", [P(SelectiveProblem)] + [vp] * 11, ctypes.c_int),
             ("ssd_gated_norm", [P(NormProblem)] + [vp] * 5, ctypes.c_int),
             ("ssd_add_norm", [P(NormProblem)] + [vp] * 7, ctypes.c_int)):
@@ -107,14 +105,19 @@ def _elsewhere(x: torch.Tensor, stream) -> bool:
     return stream is not None or not x.is_cuda or x.get_device() != _current_device()
 
 
-def _run_on(x: torch.Tensor, stream):
-    """A context in which x's device is current, and `stream` where it is given."""
+def _run_on(stream, x: torch.Tensor, *others):
+    """A context in which x's device is current, and `stream` where it is given:
+    the tensors are then recorded as used on it, so that their memory is not
+    reused before it is done."""
     if not x.is_cuda:
         raise ValueError("tensor arguments must be CUDA tensors")
     if stream is None:
         return torch.cuda.device(x.device)
     if stream.device != x.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    for t in (x, *others):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -185,7 +188,7 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("shapes: x [b,T,C], weight [C,W]")
     if _elsewhere(x, stream):
-        with _run_on(x, stream):
+        with _run_on(stream, x, weight, bias, init_states, seq_idx):
             return causal_conv(x, weight, bias, init_states, seq_idx, nseq, activation, splits, return_final_states,
                                out, final_out)
     device, dtype = x.device, x.dtype
@@ -216,7 +219,7 @@ def conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: 
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("shapes: x [b,C], weight [C,W]")
     if _elsewhere(x, stream):
-        with _run_on(x, stream):
+        with _run_on(stream, x, state, weight, bias):
             return conv_step(x, state, weight, bias, activation, splits, out)
     device, dtype = x.device, x.dtype
     b, C = x.shape
@@ -261,8 +264,7 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
                    dt_bias: Optional[torch.Tensor] = None, dt_softplus: bool = True,
                    init_states: Optional[torch.Tensor] = None, seq_idx: Optional[torch.Tensor] = None,
                    nseq: Optional[int] = None, return_final_states: bool = True, out: Optional[torch.Tensor] = None,
-                   final_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None
-                   ) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+                   final_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """The selective scan with a decay per channel and state:
 
         delta = softplus(dt + dt_bias),  h[n] <- exp(delta A[c, n]) h[n] + delta u B[n]
@@ -276,9 +278,9 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     if u.dim() != 3:
         raise ValueError("u must be [b, T, channels]")
     if _elsewhere(u, stream):
-        with _run_on(u, stream):
+        with _run_on(stream, u, dt, A, B, C, D, z, dt_bias, init_states, seq_idx):
             return selective_scan(u, dt, A, B, C, D, z, dt_bias, dt_softplus, init_states, seq_idx, nseq,
-                                  return_final_states, out, final_out, workspace)
+                                  return_final_states, out, final_out)
     dtype = _dtype(u, "u")
     ptrs, ch, N, G, strides = _selective(u, dt, A, B, C, D, z, dt_bias)
     (b, T, _), device, nseq = u.shape, u.device, _nseq(seq_idx, nseq)
@@ -292,14 +294,7 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     if return_final_states:
         final = u.new_empty(states, dtype=torch.float32) if final_out is None else final_out
         finp = _need(final, "final_out", states, torch.float32, device)
-    need = _fn.ssd_selective_scan_workspace_bytes(p)
-    if workspace is None and 0 < need < _INVALID_SIZE:
-        workspace = u.new_empty(need, dtype=torch.uint8)
-    wsp, size = None, 0
-    if workspace is not None:
-        wsp = _need(workspace, "workspace", workspace.shape, workspace.dtype, device)
-        size = workspace.numel() * workspace.element_size()
-    _ssd._check(_fn.ssd_selective_scan(p, *ptrs, initp, idsp, yp, finp, wsp, size, _raw_stream(device.index)),
+    _ssd._check(_fn.ssd_selective_scan(p, *ptrs, initp, idsp, yp, finp, _raw_stream(device.index)),
                 "ssd_selective_scan")
     return y, final
 
@@ -314,7 +309,7 @@ def selective_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     if u.dim() != 2:
         raise ValueError("u must be [b, channels]")
     if _elsewhere(u, stream):
-        with _run_on(u, stream):
+        with _run_on(stream, u, dt, A, B, C, state, D, z, dt_bias):
             return selective_step(u, dt, A, B, C, state, D, z, dt_bias, dt_softplus, out)
     dtype = _dtype(u, "u")
     ptrs, ch, N, G, strides = _selective(u, dt, A, B, C, D, z, dt_bias)
@@ -349,7 +344,7 @@ def gated_norm(x: torch.Tensor, weight: torch.Tensor, z: Optional[torch.Tensor] 
     afterwards; without z the plain norm. x and z [rows, channels] or
     [b, T, channels] in one dtype (float32 or bfloat16), which the result has too."""
     if _elsewhere(x, stream):
-        with _run_on(x, stream):
+        with _run_on(stream, x, weight, z):
             return gated_norm(x, weight, z, ngroups, eps, gate_first, out)
     dtype, device, shape = x.dtype, x.device, x.shape
     xp, zp = _need(x, "x", shape, dtype, device, False), _need(z, "z", shape, dtype, device, False)
@@ -376,7 +371,7 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     dtype (without one, r has residual_dtype, fp32 by default). The norm is taken of
     the unrounded sum. residual_out=residual updates a dense residual in place."""
     if _elsewhere(x, stream):
-        with _run_on(x, stream):
+        with _run_on(stream, x, weight, residual, scale):
             return add_norm(x, weight, residual, scale, eps, residual_dtype, out, residual_out)
     dtype, device, shape, code = x.dtype, x.device, x.shape, _dtype(x, "x")
     rdt = residual.dtype if residual is not None else (residual_dtype or torch.float32)

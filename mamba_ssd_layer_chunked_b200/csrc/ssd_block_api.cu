@@ -61,7 +61,8 @@ ssd_status check_strides(const int64_t* s, int n, int64_t batch, int64_t tokens)
 
 ssd_status check_sizes(int64_t batch, int64_t seqlen, int64_t channels) {
     if (batch < 1 || seqlen < 1 || channels < 1) return SSD_ERR_INVALID_ARG;
-    if (batch > INT32_MAX || seqlen > INT32_MAX || batch * seqlen > INT32_MAX || channels > kMaxChannels)
+    // token indices and a few tiles beyond the last one stay in 32 bits
+    if (batch > INT32_MAX || seqlen > (1 << 30) || batch * seqlen > INT32_MAX || channels > kMaxChannels)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -160,12 +161,9 @@ ssd_status check_selective(const ssd_selective_problem* p, bool step) {
     return SSD_OK;
 }
 
-size_t selective_workspace_bytes(const ssd_selective_problem*) { return 0; }
-
 ssd_status run_selective(const ssd_selective_problem* p, bool step, const void* u, const void* dt, const float* A,
                          const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
-                         const float* init, const int32_t* seq_idx, void* y, float* final_states, void* workspace,
-                         size_t workspace_bytes, void* stream) {
+                         const float* init, const int32_t* seq_idx, void* y, float* final_states, void* stream) {
     ssd_status s = check_selective(p, step);
     if (s != SSD_OK) return s;
     for (const int64_t* q : {p->u_stride, p->dt_stride, z ? p->z_stride : p->u_stride, p->B_stride, p->C_stride})
@@ -182,10 +180,8 @@ ssd_status run_selective(const ssd_selective_problem* p, bool step, const void* 
     const int64_t states = p->batch * (step ? 1 : p->nseq) * p->dstate * n, GN = p->ngroups * p->dstate;
     const Strides us(p->u_stride, step), ds(p->dt_stride, step), zs(z ? p->z_stride : p->u_stride, step), bs(p->B_stride, step),
         cs(p->C_stride, step);
-    const size_t need = step ? 0 : selective_workspace_bytes(p);
     const Span spans[] = {dense(y, rows * n, e),
                           dense(final_states, states, 4),
-                          dense(need ? workspace : nullptr, (int64_t)need, 1),
                           strided(u, p->batch, T, us.s, n, e),
                           strided(dt, p->batch, T, ds.s, n, e),
                           strided(z, p->batch, T, zs.s, n, e),
@@ -196,9 +192,7 @@ ssd_status run_selective(const ssd_selective_problem* p, bool step, const void* 
                           dense(dt_bias, n, 4),
                           dense(init, states, 4),
                           dense(seq_idx, rows, 4)};
-    if (!apart(spans, 3)) return SSD_ERR_INVALID_ARG;
-    if (need && (!aligned_to(workspace, 16) || !workspace || workspace_bytes < need))
-        return workspace && !aligned_to(workspace, 16) ? SSD_ERR_INVALID_ARG : SSD_ERR_WORKSPACE;
+    if (!apart(spans, 2)) return SSD_ERR_INVALID_ARG;
     if ((s = check_device()) != SSD_OK) return s;
     ssd::SelectiveArgs a;
     a.batch = (int)p->batch;
@@ -278,24 +272,19 @@ ssd_status ssd_conv_step(const ssd_conv_problem* p, const void* x, const float* 
     return run_conv(p, true, x, weight, bias, nullptr, nullptr, out, state, stream);
 }
 
-size_t ssd_selective_scan_workspace_bytes(const ssd_selective_problem* p) {
-    return check_selective(p, false) == SSD_OK ? selective_workspace_bytes(p) : (size_t)-1;
-}
-
 ssd_status ssd_selective_scan(const ssd_selective_problem* p, const void* u, const void* dt, const float* A,
                               const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
                               const float* init_states, const int32_t* seq_idx, void* y, float* final_states,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              void* stream) {
     TraceRange trace("ssd_selective_scan");
-    return run_selective(p, false, u, dt, A, B, C, D, z, dt_bias, init_states, seq_idx, y, final_states, workspace,
-                         workspace_bytes, stream);
+    return run_selective(p, false, u, dt, A, B, C, D, z, dt_bias, init_states, seq_idx, y, final_states, stream);
 }
 
 ssd_status ssd_selective_step(const ssd_selective_problem* p, const void* u, const void* dt, const float* A,
                               const void* B, const void* C, const float* D, const void* z, const float* dt_bias,
                               float* state, void* y, void* stream) {
     TraceRange trace("ssd_selective_step");
-    return run_selective(p, true, u, dt, A, B, C, D, z, dt_bias, nullptr, nullptr, y, state, nullptr, 0, stream);
+    return run_selective(p, true, u, dt, A, B, C, D, z, dt_bias, nullptr, nullptr, y, state, stream);
 }
 
 ssd_status ssd_gated_norm(const ssd_norm_problem* p, const void* x, const void* z, const float* weight, void* out,

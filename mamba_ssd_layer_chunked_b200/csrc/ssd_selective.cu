@@ -20,6 +20,7 @@
 // Bound by the special-function unit (one exponential per (token, channel,
 // state)) and by shared memory's B, C and delta, read once per lane.
 
+#include <atomic>
 #include <type_traits>
 
 #include "ssd_block.cuh"
@@ -542,10 +543,17 @@ cudaError_t start_scan(const SelectiveArgs& a, cudaStream_t st) {
     const int per = a.channels / a.ngroups, units = (per + Sh::CPW - 1) / Sh::CPW;
     const unsigned grid = (unsigned)((int64_t)a.batch * a.ngroups * units);
     const auto kernel = selective_scan_kernel<T, Sh, kMinCtas, kSeq, kCopy>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (smem > 48 * 1024) {  // once per device (a race only repeats it)
+        static std::atomic<uint64_t> set{0};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (!bit || !(set.load(std::memory_order_acquire) & bit)) {
+            e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+            set.fetch_or(bit, std::memory_order_release);
+        }
     }
     kernel<<<grid, 32 * Sh::K, smem, st>>>(a, units);
     return cudaGetLastError();

@@ -115,7 +115,7 @@ def step(p, x=FAKE(0), weight=FAKE(1), bias=None, state=FAKE(5), out0=FAKE(2), o
     ("width", 1, UNSUPPORTED), ("width", 5, UNSUPPORTED), ("nseq", 0, INVALID), ("nseq", 2, INVALID),
     ("dtype", 7, INVALID), ("act", 2, INVALID), ("x_stride", (-1, 96), INVALID), ("x_stride", (0, 1 << 41), UNSUPPORTED),
     ("split", (96, 1, 0), INVALID), ("split", (0, 96, 0), INVALID), ("split", (64, 0, 32), INVALID),
-    ("split", (128, -16, -16), INVALID), ("channels", 1 << 21, UNSUPPORTED), ("seqlen", 1 << 31, UNSUPPORTED),
+    ("split", (128, -16, -16), INVALID), ("channels", 1 << 21, UNSUPPORTED), ("seqlen", (1 << 30) + 1, UNSUPPORTED),
     ("batch", 1 << 30, UNSUPPORTED)])
 def test_conv_refuses_bad_problems(field, value, expect):
     assert conv(conv_problem(**{field: value})) == expect
@@ -152,9 +152,9 @@ def selective_problem(**kw):
 
 
 def scan(p, u=FAKE(0), dt=FAKE(1), A=FAKE(2), B=FAKE(3), C=FAKE(4), D=None, z=None, bias=None, init=None, seq=None,
-         y=FAKE(5), final=None, ws=None, wsb=0):
+         y=FAKE(5), final=None):
     return ssd.lib().ssd_selective_scan(None if p is None else ctypes.byref(p), u, dt, A, B, C, D, z, bias, init, seq,
-                                        y, final, ws, wsb, None)
+                                        y, final, None)
 
 
 def scan_step(p, u=FAKE(0), dt=FAKE(1), A=FAKE(2), B=FAKE(3), C=FAKE(4), D=None, z=None, bias=None, state=FAKE(6),
@@ -167,14 +167,12 @@ def scan_step(p, u=FAKE(0), dt=FAKE(1), A=FAKE(2), B=FAKE(3), C=FAKE(4), D=None,
     ("batch", 0, INVALID), ("seqlen", 0, INVALID), ("channels", 0, INVALID), ("dstate", 0, INVALID),
     ("dstate", 257, UNSUPPORTED), ("ngroups", 0, INVALID), ("ngroups", 5, INVALID), ("nseq", 0, INVALID),
     ("nseq", 3, INVALID), ("dtype", 9, INVALID), ("channels", 1 << 21, UNSUPPORTED), ("u_stride", (-4, 1), INVALID),
-    ("C_stride", (1 << 41, 0), UNSUPPORTED), ("seqlen", 1 << 32, UNSUPPORTED)])
+    ("C_stride", (1 << 41, 0), UNSUPPORTED), ("seqlen", (1 << 30) + 1, UNSUPPORTED)])
 def test_selective_refuses_bad_problems(field, value, expect):
     p = selective_problem(**{field: value})
     assert scan(p) == expect
     if field not in ("seqlen", "nseq"):
         assert scan_step(p) == expect
-    if field not in ("nseq",) and "stride" not in field:
-        assert ssd.lib().ssd_selective_scan_workspace_bytes(ctypes.byref(p)) == ctypes.c_size_t(-1).value
 
 
 @pytest.mark.parametrize("arg", ["u", "dt", "A", "B", "C", "y"])
@@ -209,7 +207,7 @@ def anorm(p, x=FAKE(0), r=FAKE(1), w=FAKE(2), s=None, out=FAKE(3), rout=FAKE(4))
     ("batch", 0, INVALID), ("seqlen", -1, INVALID), ("channels", 0, INVALID), ("ngroups", 0, INVALID),
     ("ngroups", 7, INVALID), ("dtype", 2, INVALID), ("eps", -1.0, INVALID), ("eps", float("nan"), INVALID),
     ("eps", float("inf"), INVALID), ("channels", 32769, UNSUPPORTED), ("x_stride", (0, -1), INVALID),
-    ("z_stride", (0, -1), INVALID), ("seqlen", 1 << 31, UNSUPPORTED)])
+    ("z_stride", (0, -1), INVALID), ("seqlen", (1 << 30) + 1, UNSUPPORTED)])
 def test_norms_refuse_bad_problems(field, value, expect):
     assert gnorm(norm_problem(**{field: value})) == expect
     assert anorm(norm_problem(**{field: value})) == expect

@@ -460,6 +460,16 @@ def test_stream_argument_and_given_outputs():
     st.synchronize()
     assert f is fin and all(a is b for a, b in zip(y, out))
     assert all(torch.equal(a, b) for a, b in zip(y, y0)) and torch.equal(f, f0)
+    # every operator on a given stream, its inputs dropped right after the call
+    i = on_gpu(scan_inputs(rng, 1, 40, 32, 16, 1, "bf16", True, True, True, True), (0, 0))
+    res, z, g = rand(rng, 2, 20, 32).cuda(), rand(rng, 2, 20, 32, dtype="bf16").cuda(), rand(rng, 32).cuda()
+    want = [*ssd.selective_scan(**i), ssd.gated_norm(x, g, z=z), *ssd.add_norm(x, g, res, scale=g)]
+    torch.cuda.synchronize()
+    got = [*ssd.selective_scan(**{k: v.clone() if torch.is_tensor(v) else v for k, v in i.items()}, stream=st)]
+    got.append(ssd.gated_norm(x.clone(), g.clone(), z=z.clone(), stream=st))
+    got += ssd.add_norm(x.clone(), g.clone(), res.clone(), scale=g.clone(), stream=st)
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
     y, f = ssd.causal_conv(x, w, return_final_states=False)
     assert f is None and torch.equal(y, torch.cat(y0, -1))
 
