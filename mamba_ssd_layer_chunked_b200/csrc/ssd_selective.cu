@@ -304,6 +304,14 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     };
     unsigned starts = 0u;  // sequences that start in the slice: bit t for token t
     int id = 0, id_before = -1;
+    // ids of the next slice's tokens and of those before them, as loaded (a use would wait for the load)
+    int next_id = 0, next_before = 0;
+    const auto load_ids = [&](int tw) {
+        const int t = min(tw + lane % L, a.seqlen - 1);
+        next_id = a.seq_idx[row0 + t];
+        next_before = a.seq_idx[row0 + max(t - 1, 0)];
+    };
+    const auto clamp_id = [&](int s) { return min(max(s, 0), a.nseq - 1); };
     // The slice that starts at token tw. full: it, and the slice fetched meanwhile, lie inside the row, and
     // it is not the row's last one.
     const auto prepare = [&](int tw, auto full) {
@@ -350,11 +358,11 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             fetch(tw + K * L, 0, full);
         }
         if (kSeq) {  // lane i < L looks at token tw + i
-            const int t = min(tw + lane % L, a.seqlen - 1);
-            id = seq_at(a.seq_idx, row0, t, a.nseq);
-            id_before = -1;
-            if (t > 0) id_before = seq_at(a.seq_idx, row0, t - 1, a.nseq);
-            starts = __ballot_sync(0xffffffffu, lane < L && tw + lane < a.seqlen && (t == 0 || id != id_before));
+            const int t = tw + lane % L;
+            id = clamp_id(next_id);
+            id_before = t > 0 ? clamp_id(next_before) : -1;
+            starts = __ballot_sync(0xffffffffu, lane < L && t < a.seqlen && (t == 0 || id != id_before));
+            load_ids(tw + K * L);
         }
         __syncwarp();
         // ---- a and v of the slice ----
@@ -386,20 +394,28 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             h[4 * i / S][4 * i % S / 2] = make_float2(q.x, q.y);
             h[4 * i / S][4 * i % S / 2 + 1] = make_float2(q.z, q.w);
         }
-#pragma unroll
-        for (int t = 0; t < L; ++t) {
-            if (kSeq && (starts >> t & 1u)) {
-                const int s = __shfl_sync(0xffffffffu, id, t), before = __shfl_sync(0xffffffffu, id_before, t);
-                if (a.final_states) {
-                    if (before >= 0) write_state(h, before);
-                    keep(before + 1, s);
-                }
-                init_state(h, s);
-            }
+        const auto advance = [&](int t) {
 #pragma unroll
             for (int m = 0; m < CH; ++m)
 #pragma unroll
                 for (int j = 0; j < S2; ++j) h[m][j] = hv[t][m][j] = __ffma2_rn(av[t][m][j], h[m][j], hv[t][m][j]);
+        };
+        if (!kSeq || starts == 0u) {  // a branch per token here would delay every warp of the CTA
+#pragma unroll
+            for (int t = 0; t < L; ++t) advance(t);
+        } else {
+#pragma unroll
+            for (int t = 0; t < L; ++t) {
+                if (starts >> t & 1u) {
+                    const int s = __shfl_sync(0xffffffffu, id, t), before = __shfl_sync(0xffffffffu, id_before, t);
+                    if (a.final_states) {
+                        if (before >= 0) write_state(h, before);
+                        keep(before + 1, s);
+                    }
+                    init_state(h, s);
+                }
+                advance(t);
+            }
         }
         if (full || w < K - 1 || tw + L < a.seqlen) put_state(h);  // the row's last tile ends the chain
         if (!full && a.final_states && tw < a.seqlen && tw + L >= a.seqlen) {  // this slice has the row's last token
@@ -449,6 +465,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     const int first_token = w * L, step = K * L;
     // whole: the tiles whose fetches, two tiles ahead at most, lie inside the row
     const int whole = max(0, min(a.seqlen / step - 2, tiles - 1));
+    if (kSeq) load_ids(first_token);
     prepare(first_token, std::false_type());
     int tile = 0;
     for (; tile + 1 < whole; ++tile) {
