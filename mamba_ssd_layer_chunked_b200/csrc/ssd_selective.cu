@@ -303,15 +303,13 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             unpack(*reinterpret_cast<const Pack<float, S>*>(sm_bc + i), f);
     };
     unsigned starts = 0u;  // sequences that start in the slice: bit t for token t
-    int id = 0, id_before = -1;
-    // ids of the next slice's tokens and of those before them, as loaded (a use would wait for the load)
-    int next_id = 0, next_before = 0;
-    const auto load_ids = [&](int tw) {
-        const int t = min(tw + lane % L, a.seqlen - 1);
-        next_id = a.seq_idx[row0 + t];
-        next_before = a.seq_idx[row0 + max(t - 1, 0)];
+    int id = 0, id_before = 0;
+    // The ids around the next slice: lane i <= L has that of its token i - 1 (as loaded: a use would wait).
+    int next_id = 0, id_token = w * L - 1 + min(lane, L);
+    const auto load_ids = [&]() {
+        if (id_token >= 0 && id_token < a.seqlen) next_id = a.seq_idx[row0 + id_token];
+        id_token += K * L;
     };
-    const auto clamp_id = [&](int s) { return min(max(s, 0), a.nseq - 1); };
     // The slice that starts at token tw. full: it, and the slice fetched meanwhile, lie inside the row, and
     // it is not the row's last one.
     const auto prepare = [&](int tw, auto full) {
@@ -357,12 +355,12 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             for (int i = 0; i < Sh::NB; ++i) sm_bc[lane + 32 * i] = to_f32(rbc[i]);
             fetch(tw + K * L, 0, full);
         }
-        if (kSeq) {  // lane i < L looks at token tw + i
-            const int t = tw + lane % L;
-            id = clamp_id(next_id);
-            id_before = t > 0 ? clamp_id(next_before) : -1;
-            starts = __ballot_sync(0xffffffffu, lane < L && t < a.seqlen && (t == 0 || id != id_before));
-            load_ids(tw + K * L);
+        if (kSeq) {  // lane i looks at token tw + i, and at the one before it
+            id_before = min(max(next_id, 0), a.nseq - 1);
+            id = __shfl_down_sync(0xffffffffu, id_before, 1);
+            const bool first = tw + lane == 0 || id != id_before;
+            starts = __ballot_sync(0xffffffffu, first && lane < L && (full || tw + lane < a.seqlen));
+            load_ids();
         }
         __syncwarp();
         // ---- a and v of the slice ----
@@ -409,8 +407,8 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
                 if (starts >> t & 1u) {
                     const int s = __shfl_sync(0xffffffffu, id, t), before = __shfl_sync(0xffffffffu, id_before, t);
                     if (a.final_states) {
-                        if (before >= 0) write_state(h, before);
-                        keep(before + 1, s);
+                        if (tw + t > 0) write_state(h, before);
+                        keep(tw + t > 0 ? before + 1 : 0, s);
                     }
                     init_state(h, s);
                 }
@@ -465,7 +463,7 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     const int first_token = w * L, step = K * L;
     // whole: the tiles whose fetches, two tiles ahead at most, lie inside the row
     const int whole = max(0, min(a.seqlen / step - 2, tiles - 1));
-    if (kSeq) load_ids(first_token);
+    if (kSeq) load_ids();
     prepare(first_token, std::false_type());
     int tile = 0;
     for (; tile + 1 < whole; ++tile) {
