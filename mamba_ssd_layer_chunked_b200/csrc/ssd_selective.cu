@@ -18,13 +18,14 @@
 // out. The chain is short beside the rest, so the warps work side by side
 // although the recurrence is sequential. Every exponential is formed once.
 //
-// Measured at b 1 x T 4096 x 5120 channels, N 16, bf16: 205 us (T 4096, b 4: 698).
+// Measured at b 1 x T 4096 x 5120 channels, N 16, bf16: 205 us (b 4: 698).
 // Per slice of a warp (8 channels x 8 tokens x 16 states) it issues 345 instructions,
 // 40 of them special-function, and 117 shared-memory wavefronts: 86, 80 and 117
 // cycles of an SM, against 153 that a slice takes in steady state (16 warps per
 // SM, limited by the 64 registers that a and v take) and 93 us for the
 // exponentials alone. At b 1 the 640 CTAs fill 296 places 2.2 times, so the last
-// third of the time runs on 48 SMs. Ways that measured slower: one slice per warp
+// third of the time runs on 48 SMs. Packed rows issue 424 instructions per slice
+// and spill a few registers: 317 us there with 16 sequences. Ways that measured slower: one slice per warp
 // from zero, its end state and decay exchanged by all warps (293 us: every element
 // costs two more multiplies); two channels per lane and slices of 4 at N 16 (245);
 // 4 to 7, 9 or 10 warps per CTA (231 to 320).
@@ -149,16 +150,6 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
             A2[m][j].y = n + 1 < N ? a.A[r + n + 1] * kLog2e : 0.f;
         }
     using State = float2[CH][S2];
-    const auto each_state = [&](int s, const auto& f) {  // f(m, n's pair j, which of the two, offset)
-        for (int m = 0; m < CH; ++m) {
-            const int cg = cg0 + col * CH + m;
-            if (cg >= per) break;
-            for (int j = 0; j < S; ++j) {
-                const int n = ns * S + j;
-                if (n < N) f(m, j, (((int64_t)b * a.nseq + s) * N + n) * a.channels + g * per + cg);
-            }
-        }
-    };
     const auto init_state = [&](State& h, int s) {
 #pragma unroll
         for (int m = 0; m < CH; ++m) {
@@ -187,8 +178,11 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
     };
     // ids that do not occur keep their initial state
     const auto keep = [&](int lo, int hi) {
-        for (int s = lo; s < hi; ++s)
-            each_state(s, [&](int, int, int64_t o) { a.final_states[o] = a.init ? a.init[o] : 0.f; });
+        for (int s = lo; s < hi; ++s) {
+            State h;
+            init_state(h, s);
+            write_state(h, s);
+        }
     };
 
     // ---- inputs, ahead of their use: copies into shared memory, or registers ----
