@@ -15,7 +15,7 @@
 // its inputs in the registers; other batches go token by token. Inputs are copied
 // ahead into the thread's own slots of shared memory: a register ring of the same
 // depth spilled at the 128 registers that 16 warps per SM allow. Measured at b 4 x
-// T 4096 x 5376 channels, bf16, W 4: 71 us (5.0 TB/s of x and y), 100 us without
+// T 4096 x 5376 channels, bf16, W 4: 71 us on the device (5.0 TB/s of x and y), 100 us without
 // the copies ahead, 114 us with the window in fp32 registers and scalar taps. Left
 // to the bytes' time (55 us): the taps' and first inputs' latency at each tile's
 // start, and two special-function operations per element for the silu (39 us).
