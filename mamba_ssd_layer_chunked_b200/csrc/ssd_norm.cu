@@ -128,7 +128,8 @@ cudaError_t run(const NormArgs& a, int group, int nvec, cudaStream_t st) {
 // per SM across the CTA's one synchronisation. Rows of 5120 bf16 (640 vectors,
 // 16384 rows): gated 123 us with 1 vector per thread, 92 with 2, 84 with 4 (93 % of
 // the copy bandwidth). Rows of 2560 (320 vectors) with an fp32 residual: 81 us with
-// 1 or 2, 92 with 4, whose wider rows cost occupancy.
+// 1 or 2, 92 with 4, whose wider rows cost occupancy. Rows of odd length go element by
+// element: 5001 bf16 per row 164 us with 8 per thread, 283 with 32.
 template <typename T, typename R, int V, int kMode>
 cudaError_t by_count(const NormArgs& a, int group, cudaStream_t st) {
     const int nvec = group / V;
@@ -138,7 +139,8 @@ cudaError_t by_count(const NormArgs& a, int group, cudaStream_t st) {
         if (V == 8 || nvec <= 2048) return run<T, R, V, 4, kMode>(a, group, nvec, st);
         return run<T, R, V, 32 / V, kMode>(a, group, nvec, st);
     } else {
-        if (nvec <= 4 * kNormMaxThreads) return run<T, R, V, 4, kMode>(a, group, nvec, st);
+        if (nvec <= 2048) return run<T, R, V, 4, kMode>(a, group, nvec, st);
+        if (nvec <= 8 * kNormMaxThreads) return run<T, R, V, 8, kMode>(a, group, nvec, st);
         return run<T, R, V, 32, kMode>(a, group, nvec, st);
     }
 }

@@ -25,7 +25,7 @@
 // SM, limited by the 64 registers that a and v take) and 93 us for the
 // exponentials alone. At b 1 the 640 CTAs fill 296 places 2.2 times, so the last
 // third of the time runs on 48 SMs. Packed rows issue 424 instructions per slice
-// and spill a few registers: 317 us there with 16 sequences. Ways that measured slower: one slice per warp
+// and spill a few registers: 286 us there with 16 sequences. Ways that measured slower: one slice per warp
 // from zero, its end state and decay exchanged by all warps (293 us: every element
 // costs two more multiplies); two channels per lane and slices of 4 at N 16 (245);
 // 4 to 7, 9 or 10 warps per CTA (231 to 320).
