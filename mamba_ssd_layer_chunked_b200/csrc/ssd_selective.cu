@@ -206,11 +206,13 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
 #pragma unroll
         for (int i = 0; i < Sh::TR; ++i) {  // copy v: array (u, dt, z), token, part of the token's channels
             const int v = lane + 32 * i, arr = v / (L * PT), t = v / PT % L, part = v % PT;
+            // per is a multiple of a part, so a part lies in the group or behind it. Those behind it (in the last
+            // unit) copy no bytes, but their source has to be as aligned as any: the group's first channel.
             const int cg = cg0 + part * (Sh::TB / Sh::E);
             const int64_t step = arr == 0 ? a.us_t : arr == 1 ? a.ds_t : a.zs_t;
             tstep[i] = step * (K * L);
-            tsrc[i] = (arr == 0 ? u : arr == 1 ? dt : z) + (w * L + t) * step + min(cg, per - 1);
-            tbytes[i] = min(Sh::TB, max(0, per - cg) * Sh::E);
+            tsrc[i] = (arr == 0 ? u : arr == 1 ? dt : z) + (w * L + t) * step + (cg < per ? cg : 0);
+            tbytes[i] = cg < per ? Sh::TB : 0;
             if (arr == 2 && !a.z) tbytes[i] = 0, tsrc[i] = u, tstep[i] = 0;  // no gate: zeros
             if (arr > 2) tbytes[i] = -1;
         }
