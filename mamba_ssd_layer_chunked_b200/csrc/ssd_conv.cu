@@ -273,6 +273,9 @@ __global__ void __launch_bounds__(kConvThreads, V >= 4 ? 4 : 1)
                     if (t == T_ - 1) keep(s + 1, a.nseq);
                 }
             }
+            // The batch's own copies were not read, but have to land before its slots are copied into again:
+            // copies are not ordered among each other.
+            if constexpr (kRing) copy_wait<kConvAhead - 1>();
         }
         if constexpr (kRing) {
             copy_batch(tb + kConvAhead * kConvBatch, slot);

@@ -1,14 +1,127 @@
 """The operators around the scan on the paths that their launch rules choose by
 size and alignment, against the fp64 definitions (oracle.block_oracle).
-Tolerances: those of test_block_gpu, whose derivation is at its head."""
+Tolerances: those of test_block_gpu, whose derivation is at its head. The large
+convolutions are compared on the device with a vectorised form of the definition
+in 64 bits, which a CPU test holds to the oracle's."""
 import numpy as np
 import pytest
+import torch
 
 import mamba_ssd_layer_chunked_b200 as ssd
-from tests.test_block_gpu import check_scan, cuda, ids_of, on_gpu, rand, scan_inputs, scan_reference
+from oracle import block_oracle as ref
+from tests.test_block_gpu import (DT, FP32, HALF, check_scan, cuda, ids_of, num, on_gpu, rand, scan_inputs,
+                                  scan_reference, sliced)
 
-pytestmark = pytest.mark.gpu
+# --------------------------------------------------------------------------- #
+# The short convolution: tiles of several batches
+# --------------------------------------------------------------------------- #
 
+def conv_tile(b, T, vectors):
+    """Tokens that a thread walks, in batches of 4: 32, or fewer while the threads would not fill the SMs."""
+    tile = 32
+    while tile > 4 and b * -(-T // tile) * vectors < 148 * 4 * 128:
+        tile //= 2
+    return tile
+
+
+# Sequence lengths by where they end in a tile of 32 (batches of 4): inside a batch, at a batch's edge, at a
+# tile's edge, one token apart, an absent id (0); the rest of the row is one long sequence.
+CUTS = {
+    "plain": None,
+    "in_batch": [5, 9, 21, 1, 30, 6, 23, 33],
+    "batch_edge": [4, 8, 12, 8, 16, 4, 44],
+    "tile_edge": [32, 64, 1, 31, 32],
+    "singles": [1, 1, 1, 1, 1, 1, 25, 2, 1, 30, 3, 1, 29, 1],
+    "absent": [0, 6, 0, 0, 27, 31, 0],
+    "mixed_then_whole": [2, 19, 18, 14, 12, 33, 11, 27],
+}
+
+# (channels, vectors of them per row, W, dtype, (before, after) of the slice, splits)
+ROWS = {
+    "bf16_16_bytes": (4096, 512, 4, "bf16", (8, 8), [3584, 256, 256]),
+    "f32_16_bytes": (2048, 512, 4, "f32", (4, 0), None),
+    "w3": (2048, 256, 3, "bf16", (0, 0), None),
+    "w2": (1024, 256, 2, "f32", (0, 4), [1000, 24]),
+    "bf16_pairs": (1026, 513, 4, "bf16", (2, 0), None),
+    "bf16_single": (515, 515, 4, "bf16", (1, 0), None),
+    "f32_single": (515, 515, 3, "f32", (0, 0), None),
+}
+
+
+def conv_64(x, weight, bias, init, ids, act):
+    """The definition in 64 bits for all tokens at once: (y, final windows). init [b, nseq, W-1, C]; ids may be None."""
+    x, init = x.double(), init.double()
+    (b, T, C), (nseq, back) = x.shape, init.shape[1:3]
+    t = torch.arange(T, device=x.device).expand(b, T)
+    ids = torch.zeros_like(t) if ids is None else ids.long()
+    first = torch.ones_like(ids, dtype=torch.bool)
+    first[:, 1:] = ids[:, 1:] != ids[:, :-1]
+    start = torch.where(first, t, 0).cummax(1).values
+    source = torch.cat([init.reshape(b, nseq * back, C), x], 1)  # every input and initial window of a row
+    row = torch.arange(b, device=x.device)[:, None]
+
+    def entry(k):  # where the input k tokens back is
+        return torch.where(t - k >= start, nseq * back + t - k, ids * back + back + (t - k - start))
+
+    y = torch.zeros_like(x)
+    for k in range(back + 1):
+        y += source[row, entry(k)] * weight.double()[:, back - k]
+    if bias is not None:
+        y += bias.double()
+    final = init.clone()
+    end = torch.ones_like(first)
+    end[:, :-1] = first[:, 1:]
+    r, e = end.nonzero(as_tuple=True)
+    for k in range(back):
+        final[r, ids[r, e], back - 1 - k] = source[r, entry(k)[r, e]]
+    return (y / (1 + torch.exp(-y)) if act else y), final
+
+
+@pytest.mark.parametrize("lengths", [None, [[1, 1, 0, 2, 9, 3, 0, 7], [23, 0, 0, 0, 0, 0, 0, 0]]])
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_conv_64_is_the_oracle(W, lengths):
+    rng = np.random.default_rng(W)
+    nseq = 1 if lengths is None else 8
+    x, w, bias, h0 = rand(rng, 2, 23, 5), rand(rng, 5, W), rand(rng, 5), rand(rng, 2, nseq, W - 1, 5)
+    ids = None if lengths is None else ids_of(lengths, 23)
+    for act in (False, True):
+        y, final = conv_64(x, w, bias, h0, ids, act)
+        wy, wfinal = ref.causal_conv(num(x), num(w), num(bias), num(h0), ids, nseq, act)
+        assert np.allclose(num(y), wy, rtol=1e-13, atol=1e-13) and np.array_equal(num(final), wfinal)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cuts", sorted(CUTS))
+@pytest.mark.parametrize("tile", [8, 16, 32])
+@pytest.mark.parametrize("name", sorted(ROWS))
+def test_conv_walks_tiles_of_several_batches(name, tile, cuts):
+    C, vectors, W, dt, pad, splits = ROWS[name]
+    tiles = -(-148 * 4 * 128 // vectors)
+    b, T = (1, (tiles + 2) * tile - 13) if cuts != "plain" else (2, (tiles // 2 + 2) * tile + 3)
+    assert conv_tile(b, T, vectors) == tile
+    ids, nseq = None, 1
+    if CUTS[cuts] is not None:
+        head = CUTS[cuts]
+        lengths = head + [T - 37 - sum(head), 20, 17, 0]  # the last cuts lie in the row's last tiles; an absent id
+        ids, nseq = ids_of([lengths], T).cuda(), len(lengths)
+    g = torch.Generator(device="cuda").manual_seed(C + tile)
+    normal = lambda *shape: torch.randn(shape, generator=g, device="cuda")  # noqa: E731
+    x, w, bias = normal(b, T, C).to(DT[dt]), 0.7 * normal(C, W), normal(C)
+    h0 = normal(b, nseq, W - 1, C).to(DT[dt])
+    want, wfinal = conv_64(x, w, bias, h0, ids, True)
+    size, _ = conv_64(x.abs(), w.abs(), bias.abs(), h0.abs(), ids, False)
+    y, final = ssd.causal_conv(sliced(x, *pad), w, bias, init_states=h0, seq_idx=ids, nseq=nseq, splits=splits)
+    y = torch.cat(y, -1) if splits else y
+    lim = HALF[dt] * want.abs() * (1 + 2.0 ** -7) + FP32 * size * (1 + size) + 1e-37
+    over = (y.double() - want).abs() - lim
+    at = np.unravel_index(int(over.argmax()), over.shape)
+    assert over[at] <= 0, (at, float(y[at]), float(want[at]), float(lim[at]))  # also fails on NaN
+    assert torch.equal(final.double(), wfinal)  # windows are copies of inputs
+
+
+# --------------------------------------------------------------------------- #
+# The selective scan
+# --------------------------------------------------------------------------- #
 
 def run_scan(rng, b, T, c, N, G, dt, lengths=None, pad=(0, 0), init=True):
     """selective_scan with every optional input, against its definition."""
@@ -23,6 +136,7 @@ def run_scan(rng, b, T, c, N, G, dt, lengths=None, pad=(0, 0), init=True):
 
 # Aligned rows (copied 16 bytes at a time) whose last unit of channels is partial: a warp takes 8 channels
 # with 9 to 16 states, 16 with fewer, and one copy holds 4 (fp32) or 8 (bf16) of them.
+@pytest.mark.gpu
 @pytest.mark.parametrize("packed", [False, True])
 @pytest.mark.parametrize("c,N,G,dt", [(12, 16, 1, "f32"), (4, 12, 1, "f32"), (1540, 16, 1, "f32"), (24, 16, 2, "f32"),
                                       (20, 8, 1, "f32"), (24, 8, 1, "f32"), (28, 4, 1, "f32"), (2436, 8, 1, "f32"),
