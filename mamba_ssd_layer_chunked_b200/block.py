@@ -6,7 +6,7 @@ Activations may be slices of a projection's output: their last dimension is
 contiguous, the others may have any stride. Every call runs on the device of its
 tensors and on that device's current torch stream, or on ``stream``; outputs are
 allocated on the stream the call runs on. Inputs must be ready on that stream;
-their memory is kept until it is done with them.
+the memory of inputs and of given outputs is kept until it is done with them.
 """
 from __future__ import annotations
 
@@ -107,8 +107,9 @@ def _elsewhere(x: torch.Tensor, stream) -> bool:
 
 def _run_on(stream, x: torch.Tensor, *others):
     """A context in which x's device is current, and `stream` where it is given:
-    the tensors are then recorded as used on it, so that their memory is not
-    reused before it is done."""
+    the call's tensors, given outputs among them (tensors or tuples of tensors),
+    are then recorded as used on it, so that their memory is not reused before it
+    is done."""
     if not x.is_cuda:
         raise ValueError("tensor arguments must be CUDA tensors")
     if stream is None:
@@ -116,8 +117,9 @@ def _run_on(stream, x: torch.Tensor, *others):
     if stream.device != x.device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
     for t in (x, *others):
-        if isinstance(t, torch.Tensor) and t.is_cuda:
-            t.record_stream(stream)
+        for v in t if isinstance(t, (tuple, list)) else (t,):
+            if isinstance(v, torch.Tensor) and v.is_cuda:
+                v.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -188,7 +190,7 @@ def causal_conv(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     if x.dim() != 3 or weight.dim() != 2:
         raise ValueError("shapes: x [b,T,C], weight [C,W]")
     if _elsewhere(x, stream):
-        with _run_on(stream, x, weight, bias, init_states, seq_idx):
+        with _run_on(stream, x, weight, bias, init_states, seq_idx, out, final_out):
             return causal_conv(x, weight, bias, init_states, seq_idx, nseq, activation, splits, return_final_states,
                                out, final_out)
     device, dtype = x.device, x.dtype
@@ -219,7 +221,7 @@ def conv_step(x: torch.Tensor, state: torch.Tensor, weight: torch.Tensor, bias: 
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("shapes: x [b,C], weight [C,W]")
     if _elsewhere(x, stream):
-        with _run_on(stream, x, state, weight, bias):
+        with _run_on(stream, x, state, weight, bias, out):
             return conv_step(x, state, weight, bias, activation, splits, out)
     device, dtype = x.device, x.dtype
     b, C = x.shape
@@ -278,7 +280,7 @@ def selective_scan(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     if u.dim() != 3:
         raise ValueError("u must be [b, T, channels]")
     if _elsewhere(u, stream):
-        with _run_on(stream, u, dt, A, B, C, D, z, dt_bias, init_states, seq_idx):
+        with _run_on(stream, u, dt, A, B, C, D, z, dt_bias, init_states, seq_idx, out, final_out):
             return selective_scan(u, dt, A, B, C, D, z, dt_bias, dt_softplus, init_states, seq_idx, nseq,
                                   return_final_states, out, final_out)
     dtype = _dtype(u, "u")
@@ -309,7 +311,7 @@ def selective_step(u: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.
     if u.dim() != 2:
         raise ValueError("u must be [b, channels]")
     if _elsewhere(u, stream):
-        with _run_on(stream, u, dt, A, B, C, state, D, z, dt_bias):
+        with _run_on(stream, u, dt, A, B, C, state, D, z, dt_bias, out):
             return selective_step(u, dt, A, B, C, state, D, z, dt_bias, dt_softplus, out)
     dtype = _dtype(u, "u")
     ptrs, ch, N, G, strides = _selective(u, dt, A, B, C, D, z, dt_bias)
@@ -344,7 +346,7 @@ def gated_norm(x: torch.Tensor, weight: torch.Tensor, z: Optional[torch.Tensor] 
     afterwards; without z the plain norm. x and z [rows, channels] or
     [b, T, channels] in one dtype (float32 or bfloat16), which the result has too."""
     if _elsewhere(x, stream):
-        with _run_on(stream, x, weight, z):
+        with _run_on(stream, x, weight, z, out):
             return gated_norm(x, weight, z, ngroups, eps, gate_first, out)
     dtype, device, shape = x.dtype, x.device, x.shape
     xp, zp = _need(x, "x", shape, dtype, device, False), _need(z, "z", shape, dtype, device, False)
@@ -371,7 +373,7 @@ def add_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Ten
     dtype (without one, r has residual_dtype, fp32 by default). The norm is taken of
     the unrounded sum. residual_out=residual updates a dense residual in place."""
     if _elsewhere(x, stream):
-        with _run_on(stream, x, weight, residual, scale):
+        with _run_on(stream, x, weight, residual, scale, out, residual_out):
             return add_norm(x, weight, residual, scale, eps, residual_dtype, out, residual_out)
     dtype, device, shape, code = x.dtype, x.device, x.shape, _dtype(x, "x")
     rdt = residual.dtype if residual is not None else (residual_dtype or torch.float32)
