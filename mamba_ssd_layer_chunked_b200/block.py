@@ -96,8 +96,10 @@ def _need(t: Optional[torch.Tensor], name: str, shape, dtype, device, dense=True
     return t.data_ptr()
 
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# torch's own calls behind the public ones, which cost several times as much per call; a torch built without
+# CUDA has neither, and no tensor that would reach them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _elsewhere(x: torch.Tensor, stream) -> bool:

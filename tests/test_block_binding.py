@@ -1,5 +1,9 @@
 """The binding of the operators around the scan: which tensors a call on a given
 stream keeps, and what importing it needs."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -94,3 +98,24 @@ def test_memory_of_dropped_outputs_waits_for_the_stream(name):
     side.synchronize()
     later = [torch.empty(n, dtype=torch.float32, device="cuda") for n in sizes]
     assert where & {m.data_ptr() for m in later}  # they had been dropped: now they are handed out
+
+
+def test_import_and_refusals_need_no_cuda_build_of_torch():
+    """Without the functions that only a CUDA build of torch has, the package imports and refuses CPU tensors."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import mamba_ssd_layer_chunked_b200 as ssd
+try:
+    ssd.gated_norm(torch.zeros(2, 8), torch.zeros(8))
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise AssertionError("not refused")
+print("refused")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
