@@ -9,7 +9,7 @@ import torch
 
 import mamba_ssd_layer_chunked_b200 as ssd
 from oracle import block_oracle as ref
-from tests.test_block_gpu import (DT, FP32, HALF, check_scan, cuda, ids_of, num, on_gpu, rand, scan_inputs,
+from tests.test_block_gpu import (DT, FP32, HALF, check_scan, close, cuda, ids_of, num, on_gpu, rand, scan_inputs,
                                   scan_reference, sliced)
 
 # --------------------------------------------------------------------------- #
@@ -144,3 +144,25 @@ def run_scan(rng, b, T, c, N, G, dt, lengths=None, pad=(0, 0), init=True):
 def test_scan_of_partial_units(c, N, G, dt, packed):
     T = 77
     run_scan(np.random.default_rng(c + N), 1, T, c, N, G, dt, [[30, 47]] if packed else None)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_step_size_keeps_its_relative_accuracy(dt):
+    """u = B = C = 1 and A = 0: one token's state is delta = softplus(dt + dt_bias). Relative error, counted in 2^-24:
+    exponential 2, reciprocal 2, the sum 2 + e, the product, the series (2) and its last multiply-add 1 each: below
+    the 16 of FP32, from e near 1 to e near the smallest normal number."""
+    c = 4096
+    step = torch.linspace(-85.0, 30.0, c).to(DT[dt])
+    bias = torch.linspace(0.0, 0.5, c)
+    z = (step.float() + bias).double().numpy()  # the sum, rounded as the kernel rounds it
+    one = lambda *shape: torch.ones(shape, dtype=DT[dt], device="cuda")  # noqa: E731
+    A, zero = torch.zeros(c, 1, device="cuda"), torch.zeros(1, 1, c, device="cuda")
+    want = ref.softplus(z)
+    y, final = ssd.selective_scan(one(1, 1, c), step.cuda().view(1, 1, c), A, one(1, 1, 1, 1), one(1, 1, 1, 1),
+                                  dt_bias=bias.cuda())
+    ys = ssd.selective_step(one(1, c), step.cuda().view(1, c), A, one(1, 1, 1), one(1, 1, 1), zero, dt_bias=bias.cuda())
+    for state in (final, zero):
+        close(state.view(-1), want, FP32 * want, "f32", "delta")
+    for out in (y, ys):
+        close(out.view(-1), want, FP32 * want, dt, "y")
