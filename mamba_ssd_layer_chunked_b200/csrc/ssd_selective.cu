@@ -31,6 +31,7 @@
 // 4 to 7, 9 or 10 warps per CTA (231 to 320).
 
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "ssd_block.cuh"
@@ -71,6 +72,10 @@ __device__ __forceinline__ float softplus(float z) {
     s = fmaf(s, q, 1.f);
     return fmaf(2.f * r, s, z < 0.f ? 0.f : z);
 }
+
+// A rate of -infinity (a state without memory) as the lowest finite one: its decay is 0 at every step size
+// that is not 0 all the same, and 1, not NaN, at the tokens behind a row's end, whose step size is 0.
+__device__ __forceinline__ float finite_rate(float A2) { return A2 < -FLT_MAX ? -FLT_MAX : A2; }
 
 constexpr int kStages = 3;  // slices of raw inputs in shared memory: two in flight behind the current one
 
@@ -161,8 +166,8 @@ __global__ void __launch_bounds__(32 * Sh::K, kMinCtas) selective_scan_kernel(co
         for (int j = 0; j < S2; ++j) {
             const int n = ns * S + 2 * j;
             const int64_t r = (int64_t)(g * per + min(cg0 + col * CH + m, per - 1)) * N;
-            A2[m][j].x = n < N ? a.A[r + n] * kLog2e : 0.f;
-            A2[m][j].y = n + 1 < N ? a.A[r + n + 1] * kLog2e : 0.f;
+            A2[m][j].x = n < N ? finite_rate(a.A[r + n] * kLog2e) : 0.f;
+            A2[m][j].y = n + 1 < N ? finite_rate(a.A[r + n + 1] * kLog2e) : 0.f;
         }
     using State = float2[CH][S2];
     const auto init_state = [&](State& h, int s) {

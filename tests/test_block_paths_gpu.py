@@ -166,3 +166,21 @@ def test_step_size_keeps_its_relative_accuracy(dt):
         close(state.view(-1), want, FP32 * want, "f32", "delta")
     for out in (y, ys):
         close(out.view(-1), want, FP32 * want, dt, "y")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("T", [1, 13, 77, 300])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_decays_of_minus_infinity(dt, T, packed):
+    """A state with A = -inf forgets all but the last token, whatever the row's length."""
+    b, c, N = 1, 32, 16
+    rng = np.random.default_rng(T)
+    i = scan_inputs(rng, b, T, c, N, 1, dt, True, True, True, True)
+    i["A"][:, ::3] = -np.inf
+    lengths = [T // 3, T - T // 3, 0] if packed else None
+    nseq = 3 if packed else 1
+    ids, h0 = ids_of([lengths], T) if packed else None, rand(rng, b, nseq, N, c)
+    want = scan_reference(i, init_states=num(h0), seq_idx=ids, nseq=nseq)
+    y, final = ssd.selective_scan(**on_gpu(i, (0, 0)), init_states=cuda(h0), seq_idx=cuda(ids), nseq=nseq)
+    check_scan(y, final, want, i, dt)
