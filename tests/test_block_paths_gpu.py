@@ -184,3 +184,113 @@ def test_decays_of_minus_infinity(dt, T, packed):
     want = scan_reference(i, init_states=num(h0), seq_idx=ids, nseq=nseq)
     y, final = ssd.selective_scan(**on_gpu(i, (0, 0)), init_states=cuda(h0), seq_idx=cuda(ids), nseq=nseq)
     check_scan(y, final, want, i, dt)
+
+
+# --------------------------------------------------------------------------- #
+# The scan's shapes: states per lane, warps per CTA, copied and plain loads
+# --------------------------------------------------------------------------- #
+
+# states -> (channels of a warp, CTAs up to which one has more warps, tokens that the CTA's warps take in turn
+# then, and else)
+SHAPES = {8: (16, 148, 128, 64), 16: (8, 148, 128, 64), 24: (4, 148, 128, 64), 32: (4, 148, 128, 64),
+          64: (4, 296, 32, 16), 128: (2, 296, 32, 16), 200: (2, 0, 16, 16)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("copied", [True, False])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("N", sorted(SHAPES))
+def test_scan_shapes(N, many, dt, packed, copied):
+    """Rows of six turns of a CTA's warps and a rest: the loop without guards runs, and its ends. Rows aligned to 16
+    bytes are copied ahead, others (an odd offset and stride) loaded element by element."""
+    warp, few, turn, turn_many = SHAPES[N]
+    G = 2 if many and packed else 1
+    c = (few // G + 2) * G * warp if many else 3 * warp
+    T = 6 * (turn_many if many else turn) + 13
+    assert not many or c // warp > few
+    lengths = [[T // 3, 1, 1, 5, T - T // 3 - 7 - 9, 0, 9]] if packed else None
+    run_scan(np.random.default_rng(N + T), 1, T, c, N, G, dt, lengths, (0, 0) if copied else (1, 0))
+
+
+# --------------------------------------------------------------------------- #
+# Values and ids at the edges of the contract
+# --------------------------------------------------------------------------- #
+
+def same(a, b):
+    """Bitwise, whatever the values."""
+    kind = {2: torch.int16, 4: torch.int32}[a.element_size()]
+    return a.view(kind) == b.view(kind)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("N", [5, 16])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_non_finite_inputs_of_the_scan_stay_in_their_sequence(dt, N, bad):
+    """A NaN or infinity of u or dt at one token: other channels, rows, sequences and earlier tokens keep every bit."""
+    b, T, c, t0, c0 = 2, 90, 40, 40, 11
+    rng = np.random.default_rng(N)
+    i = scan_inputs(rng, b, T, c, N, 1, dt, True, True, True, True)
+    ids = ids_of([[30, 35, 25]] * b, T).cuda()
+    h0 = rand(rng, b, 3, N, c).cuda()
+    y0, f0 = ssd.selective_scan(**on_gpu(i, (0, 0)), init_states=h0, seq_idx=ids, nseq=3)
+    for name in ("u", "dt"):
+        if name == "dt" and bad == -float("inf"):
+            continue  # a step size of 0, an ordinary value
+        j = dict(i, **{name: i[name].clone()})
+        j[name][1, t0, c0] = bad
+        y, f = ssd.selective_scan(**on_gpu(j, (0, 0)), init_states=h0, seq_idx=ids, nseq=3)
+        touched = torch.zeros_like(y, dtype=torch.bool)
+        touched[1, t0:65, c0] = True
+        assert (same(y, y0) | touched).all() and not torch.isfinite(y[1, t0, c0])
+        ftouched = torch.zeros_like(f, dtype=torch.bool)
+        ftouched[1, 1, :, c0] = True
+        assert (same(f, f0) | ftouched).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_non_finite_inputs_of_the_others_stay_where_they_belong(dt):
+    b, T, c, W = 2, 50, 64, 4
+    rng = np.random.default_rng(1)
+    x, w, bias = rand(rng, b, T, c, dtype=dt).cuda(), rand(rng, c, W).cuda(), rand(rng, c).cuda()
+    z, res = rand(rng, b, T, c, dtype=dt).cuda(), rand(rng, b, T, c).cuda()
+    ids = ids_of([[22, 28]] * b, T).cuda()
+    bad = x.clone()
+    bad[1, 20, 7] = float("nan")  # two tokens before its sequence's end
+    bad[0, 5, 3] = float("inf")
+    run = lambda v: (*ssd.causal_conv(v, w, bias, seq_idx=ids, nseq=2), ssd.gated_norm(v, bias, z=z, ngroups=4),  # noqa: E731
+                     *ssd.add_norm(v, bias, res))
+    (y0, f0, g0, a0, r0), (y, f, g, a, r) = run(x), run(bad)
+    touched = torch.zeros_like(y, dtype=torch.bool)
+    touched[1, 20:22, 7] = touched[0, 5:9, 3] = True
+    assert (same(y, y0) | touched).all() and torch.isnan(y[1, 20:22, 7]).all()
+    ftouched = torch.zeros_like(f, dtype=torch.bool)
+    ftouched[1, 0, 1, 7] = True  # the sequence's last three inputs: tokens 19 to 21
+    assert (same(f, f0) | ftouched).all() and torch.isnan(f[1, 0, 1, 7])
+    rows = torch.zeros_like(y, dtype=torch.bool)
+    rows[1, 20] = rows[0, 5] = True
+    assert (same(a, a0) | rows).all()
+    element = torch.zeros_like(rows)
+    element[1, 20, 7] = element[0, 5, 3] = True
+    assert (same(r, r0) | element).all()
+    groups = torch.zeros_like(rows)
+    groups[1, 20, :16] = groups[0, 5, :16] = True  # 4 groups of 16 channels
+    assert (same(g, g0) | groups).all()
+
+
+@pytest.mark.gpu
+def test_ids_out_of_range_count_as_the_nearest_one():
+    b, T, c, N = 1, 75, 32, 16
+    rng = np.random.default_rng(3)
+    ids = ids_of([[10, 20, 45]], T)
+    wild = ids.clone()
+    wild[0, :10] = torch.tensor([-1, -2 ** 31, 0, -7, 0, -1, -1, 0, 0, -3])
+    wild[0, 30:] = torch.where(torch.arange(45) % 3 == 0, 2, 2 ** 31 - 1 - torch.arange(45)).int()
+    i = on_gpu(scan_inputs(rng, b, T, c, N, 1, "f32", True, True, True, True), (0, 0))
+    x, w = rand(rng, b, T, c).cuda(), rand(rng, c, 4).cuda()
+    for f in (lambda s: ssd.selective_scan(**i, seq_idx=s, nseq=3), lambda s: ssd.causal_conv(x, w, seq_idx=s, nseq=3)):
+        for got, want in zip(f(wild.cuda()), f(ids.cuda())):
+            assert torch.equal(got, want)
