@@ -18,15 +18,18 @@
 // out. The chain is short beside the rest, so the warps work side by side
 // although the recurrence is sequential. Every exponential is formed once.
 //
-// Measured at b 1 x T 4096 x 5120 channels, N 16, bf16: 205 us (b 4: 698).
-// Per slice of a warp (8 channels x 8 tokens x 16 states) it issues 345 instructions,
-// 40 of them special-function, and 117 shared-memory wavefronts: 86, 80 and 117
-// cycles of an SM, against 153 that a slice takes in steady state (16 warps per
-// SM, limited by the 64 registers that a and v take) and 93 us for the
-// exponentials alone. At b 1 the 640 CTAs fill 296 places 2.2 times, so the last
-// third of the time runs on 48 SMs. Packed rows issue 424 instructions per slice
-// and spill a few registers: 286 us there with 16 sequences. Ways that measured slower: one slice per warp
-// from zero, its end state and decay exchanged by all warps (293 us: every element
+// Measured at b 1 x T 4096 x 5120 channels, N 16, bf16: 207 us (b 4: 711).
+// Per slice of a warp (8 channels x 8 tokens x 16 states) it issues 355 instructions,
+// 40 of them special-function, and 117 shared-memory wavefronts: 89, 80 and 117
+// cycles of an SM, against about 155 that a slice takes in steady state: shared memory
+// is the busiest, and 16 warps per SM (limited by the 64 registers that a and v
+// take) do not cover its latency. The special functions alone would take 90 us,
+// those of the states 72. The 640 units of 8 channels are 5 on 48 SMs and 4 on the
+// others: the rules below ask whether the SMs are filled once, not how full the last
+// turn is. Packed rows issue 427 instructions and 125 wavefronts per slice: 278 us
+// with 16 sequences. Stack for spilled registers at 16 states, copied rows: none in
+// bf16, 40 bytes in fp32 (packed: 16 and 8); the most without copies at 256 states,
+// 216 bytes. Ways that measured slower: one slice per warp from zero, its end state and decay exchanged by all warps (293 us: every element
 // costs two more multiplies); two channels per lane and slices of 4 at N 16 (245);
 // 4 to 7, 9 or 10 warps per CTA (231 to 320).
 
@@ -497,9 +500,11 @@ constexpr int kStepStates = 16;  // states of a thread in flight per row
 
 // One token: a thread takes one channel of a batch row, kStepStates states at a
 // time; a CTA's channels lie in one group, whose B and C rows it keeps in shared
-// memory. Bound by the state's bytes, read and written once: 64 rows x 5120 channels
-// x 16 states take 15 us back to back (3.0 TB/s; the bytes' time is 7 us). Two rows
-// per thread took longer (29 us cold against 25).
+// memory. 64 rows x 5120 channels x 16 states take 12.4 us in a graph of steps on
+// different states (3.6 TB/s; the bytes' time is 7 us), 256 rows 42 (4.2 TB/s), and 3 rows x
+// 1536 channels 2.3; a call from Python takes 15 to 16 us whatever the size up to 64 rows. Bound by the
+// latency of the state's loads: 2560 CTAs at 5 per SM are 3.5 turns, 27 % of the warps are
+// resident and the issue slots are used at 39 %. Two rows per thread took longer (29 us cold against 25).
 // kVec: A's rows allow 16-byte loads; kWhole: N is a multiple of kStepStates.
 // Offsets within a row's state (at most 2^20 x 256 floats, 1 GB) are 32 bits from a
 // CTA-wide base: with 64-bit addresses per access their arithmetic was most of
