@@ -29,9 +29,10 @@
 // turn is. Packed rows issue 427 instructions and 125 wavefronts per slice: 278 us
 // with 16 sequences. Stack for spilled registers at 16 states, copied rows: none in
 // bf16, 40 bytes in fp32 (packed: 16 and 8); the most without copies at 256 states,
-// 216 bytes. Ways that measured slower: one slice per warp from zero, its end state and decay exchanged by all warps (293 us: every element
-// costs two more multiplies); two channels per lane and slices of 4 at N 16 (245);
-// 4 to 7, 9 or 10 warps per CTA (231 to 320).
+// 216 bytes. Ways that measured slower: one slice per warp from zero, its end state
+// and decay exchanged by all warps (293 us: every element costs two more
+// multiplies); two channels per lane and slices of 4 at N 16 (245); 4 to 7, 9 or 10
+// warps per CTA (231 to 320).
 
 #include <atomic>
 #include <cfloat>
